@@ -291,6 +291,138 @@ int moed_bench_copy(const void *src, void *dst, size_t bytes, void *stream);
 int moed_bench_read_cfg(const void *src, size_t bytes, void *sink, size_t sink_bytes, int unroll,
                         int waves_per_group, int groups, void *stream);
 
+/*
+ * The MoE block for prompts. A decode step brings a few tokens and goes through
+ * moe_decode(); a prompt brings thousands, and the weights are then read once
+ * for all rows of an expert:
+ *   moe_norm     residual addition, root-mean-square norm, optional MXFP8 copy
+ *   moe_route    (above) router logits -> topk_ids, topk_w
+ *   moe_group    the B*k routed slots sorted by expert
+ *   moe_grouped_gate_up, moe_grouped_matmul
+ *                the experts' products over the sorted, ragged rows
+ *   moe_combine  each token's k rows summed with its routing weights
+ * moe_prefill() runs the last four as one call. They are inference operators
+ * like the rest of the library: no gradients. The conventions at the top of
+ * this file hold, and these: B (tokens) is below 2^22; activations are
+ * BFLOAT16, or MXFP8 as codes [rows][K] with scales [rows][K/32].
+ *
+ * The products sum in float32 with the matrix instructions. With MXFP8
+ * activations, codes and block scales enter them as stored and every product
+ * is exact, for every scale. With BFLOAT16 activations weights are decoded to
+ * BFLOAT16 with the block scale folded in, which is exact in the range of
+ * scale codes given at moe_decode(). Results are deterministic; how rows are
+ * tiled goes by the call's sizes, so a row's low bits can differ between calls
+ * of different sizes.
+ */
+typedef enum {
+    MOED_ROWS_BF16 = 0,      /* bfloat16                                         */
+    MOED_ROWS_F32 = 1,       /* float32 (outputs only)                           */
+    MOED_ROWS_MXFP8 = 2      /* E4M3 codes and, in a tensor of their own, one
+                                UE8M0 scale per 32 of a row                      */
+} moed_rows;
+
+/*
+ * s = x + residual in float32; residual_out = s rounded to the residual's type;
+ * y[b][h] = s[b][h] / sqrt(mean_h s[b]^2 + eps) * gain[h]  (of the unrounded s).
+ *   x             [B][H] x_dtype (moed_dtype)
+ *   residual      [B][H] residual_dtype, or NULL: s = x
+ *   gain          [H] gain_dtype
+ *   residual_out  [B][H] residual_dtype, or NULL: not stored (must be NULL
+ *                 without a residual); may be the residual itself, or x where
+ *                 the types agree
+ *   out           [B][H] out_dtype, y rounded once, or NULL; may be x or the
+ *                 residual where the types agree
+ *   out_q, out_s  y in MXFP8, [B][H] codes and [B][H/32] scales, or both NULL
+ * out, or out_q and out_s, must be given. MXFP8 rule: the scale code of a
+ * block of 32 is max(floor(log2 amax) - 8 + 127, 0), 0 for a block of zeros;
+ * codes are y / 2^(scale-127) saturated to +-448 and rounded to nearest even;
+ * a block that holds an infinity or a NaN gets scale 255 and NaN codes.
+ * Limits (MOED_ERR_SHAPE): 1 <= H <= 32768, eps >= 0; H a multiple of 32 with
+ * out_q. Pointers of x, residual, gain, residual_out, out and out_q are
+ * 16-byte aligned (MOED_ERR_ALIGN). B = 0 launches nothing.
+ */
+int moe_norm(const void *x, int x_dtype, const void *residual, int residual_dtype,
+             const void *gain, int gain_dtype, float eps, void *residual_out,
+             void *out, int out_dtype, uint8_t *out_q, uint8_t *out_s,
+             int B, int H, void *stream);
+
+/*
+ * The B*k routed slots t = b*k + j sorted by expert, slots of one expert in
+ * increasing t:
+ *   offsets   [E+1] int32: expert e has the places offsets[e]..offsets[e+1]-1
+ *   order     [B*k] int32: slot of each place (-1 from place offsets[E] on)
+ *   position  [B][k] int32: place of each slot
+ * An id outside [0, E) has no place: its position is -1, which moe_combine()
+ * turns into NaN outputs of the token. workspace: at least
+ * moe_group_workspace_bytes(B, k, E) bytes, 4-byte aligned (NULL where that is
+ * 0). Limits (MOED_ERR_SHAPE): 1 <= k <= 64, 1 <= E <= 2048, B*k < 2^28. B = 0
+ * writes offsets only.
+ */
+size_t moe_group_workspace_bytes(int B, int k, int E);
+int moe_group(const int32_t *topk_ids, int B, int k, int E, int32_t *order,
+              int32_t *position, int32_t *offsets, void *workspace,
+              size_t workspace_bytes, void *stream);
+
+/*
+ * Products of sorted rows with their expert's matrices. Row r of expert e
+ * (offsets[e] <= r < offsets[e+1]) reads a[order[r] / k], or a[r] with
+ * order = NULL:
+ *   gate_up: out[r][n] = SiLU(Wg^[e][n] . a) * (Wu^[e][n] . a)
+ *   matmul:  out[r][n] = W^[e][n] . a
+ *   a        [n_a][K] a_rows: MOED_ROWS_BF16, or MOED_ROWS_MXFP8 with a_s
+ *            [n_a][K/32] (NULL for bfloat16)
+ *   order    [R] int32 or NULL (then n_a >= R); an entry outside [0, n_a*k)
+ *            makes the row NaN
+ *   offsets  [E+1] int32, non-decreasing, from 0 to at most R. Other values
+ *            give wrong rows but no access outside the tensors
+ *   w_q, w_s [E][N][K] codes ([E][N][K/2] for MOED_MXFP4), [E][N][K/32] scales
+ *   out      [R][N] out_rows (gate_up: any moed_rows; matmul: BF16 or F32)
+ *   out_s    [R][N/32] for MOED_ROWS_MXFP8 (the rule of moe_norm), else NULL
+ * Rows from offsets[E] on stay as they were. out may not overlap a. Limits
+ * (MOED_ERR_SHAPE): K and N positive multiples of 32, below 2^20; E <= 2048;
+ * R and n_a below 2^28; k >= 1. a, out and the code pointers are 16-byte
+ * aligned (MOED_ERR_ALIGN). R = 0 launches nothing.
+ */
+int moe_grouped_gate_up(const void *a, const uint8_t *a_s, int a_rows, int n_a,
+                        const int32_t *order, int k, const int32_t *offsets,
+                        const uint8_t *wg_q, const uint8_t *wg_s,
+                        const uint8_t *wu_q, const uint8_t *wu_s, int weight_format,
+                        void *out, uint8_t *out_s, int out_rows,
+                        int R, int E, int K, int N, void *stream);
+int moe_grouped_matmul(const void *a, const uint8_t *a_s, int a_rows, int n_a,
+                       const int32_t *order, int k, const int32_t *offsets,
+                       const uint8_t *w_q, const uint8_t *w_s, int weight_format,
+                       void *out, int out_rows, int R, int E, int K, int N, void *stream);
+
+/*
+ * out[b][h] = sum_j topk_w[b][j] * y[position[b][j]][h], j in increasing order
+ * in one float32 accumulator. y [R][H] y_dtype; out [B][H] out_dtype. A position
+ * outside [0, R) makes the token's outputs NaN. Limits (MOED_ERR_SHAPE):
+ * 1 <= k <= 64, 1 <= H < 2^20, R below 2^28. y and out are 16-byte aligned
+ * (MOED_ERR_ALIGN). B = 0 launches nothing.
+ */
+int moe_combine(const void *y, int y_dtype, int R, const int32_t *position,
+                const float *topk_w, void *out, int out_dtype, int B, int k, int H,
+                void *stream);
+
+/*
+ * The whole layer for prompts: moe_group, moe_grouped_gate_up,
+ * moe_grouped_matmul, moe_combine on `stream`. Arguments as moe_decode(),
+ * besides: x [B][H] x_rows (MOED_ROWS_BF16, or MOED_ROWS_MXFP8 with x_s
+ * [B][H/32]). The intermediate is kept in the type of x (MXFP8 stays MXFP8, by
+ * the rule of moe_norm), the experts' rows in out_dtype. Ids outside [0, E)
+ * make the token's outputs NaN; MOED_CHECK works as for moe_decode(). Limits:
+ * those of the four calls. workspace: at least moe_prefill_workspace_bytes(...)
+ * bytes (0 for invalid arguments), 16-byte aligned.
+ */
+size_t moe_prefill_workspace_bytes(int B, int E, int k, int H, int I, int x_rows, int out_dtype);
+int moe_prefill(const void *x, const uint8_t *x_s, int x_rows, const int32_t *topk_ids,
+                const float *topk_w, const uint8_t *wg_q, const uint8_t *wg_s,
+                const uint8_t *wu_q, const uint8_t *wu_s,
+                const uint8_t *wd_q, const uint8_t *wd_s, int weight_format,
+                void *out, int out_dtype, int B, int E, int k, int H, int I,
+                void *workspace, size_t workspace_bytes, void *stream);
+
 /* Human-readable name of a moed_status value. Never NULL. */
 const char *moed_status_string(int status);
 

@@ -1,0 +1,221 @@
+// Routed slots sorted by expert: for ids[t], t = b*k + j, the stable counting
+// sort order (slots of expert 0 first, each expert's in increasing t), every
+// slot's place in it, and where each expert's slots begin.
+//
+// Slots are taken in blocks of 16 wavefronts; a wavefront owns PER*64
+// consecutive slots and takes them 64 at a time. Lanes with the same id are
+// found with one ballot per id bit, so a slot's rank among its wavefront's
+// earlier slots of the expert is a count in LDS plus a popcount: no atomics,
+// no dependence on the order in which wavefronts run. Counts of wavefronts
+// (and, past one block, of blocks) are then summed in slot order.
+//
+// One block covers n <= 8192 slots in one launch (bound by its few barriers
+// and round trips). Larger lists take two launches: the blocks' counts to the
+// workspace, then every block adds up the counts itself (blocks*E words out
+// of L2), which costs less than a launch in between would.
+#include "launch.h"
+#include "mx_device.h"
+
+namespace moed {
+
+namespace {
+
+constexpr int kGroupThreads = 1024;
+constexpr int kGroupWavesN = kGroupThreads / kWave;
+
+// Lanes of the wavefront that hold the same id (ids < 2^bits), among `live`.
+__device__ __forceinline__ unsigned long long same_id(int id, int bits, unsigned long long live)
+{
+    unsigned long long m = live;
+    for (int i = 0; i < bits; ++i) {
+        const unsigned long long b = __ballot((id >> i) & 1);
+        m &= ((id >> i) & 1) ? b : ~b;
+    }
+    return m;
+}
+
+// Sum of v over the threads before this one, and over all (block of 1024).
+__device__ __forceinline__ int block_exclusive(int v, int* wsum, int& total)
+{
+    const int lane = threadIdx.x % kWave, w = threadIdx.x / kWave;
+    int inc = v;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+        const int o = __shfl_up(inc, d);
+        if (lane >= d)
+            inc += o;
+    }
+    if (lane == kWave - 1)
+        wsum[w] = inc;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int q = 0; q < kGroupWavesN; ++q) {
+        const int c = wsum[q];
+        before += q < w ? c : 0;
+        all += c;
+    }
+    __syncthreads();
+    total = all;
+    return before + inc - v;
+}
+
+}  // namespace
+
+// Counts of one block's slots per expert, to the workspace: counts[block][E].
+template <int PER>
+__global__ void __launch_bounds__(kGroupThreads)
+moe_group_count_kernel(const int32_t* ids, int n, int E, int32_t* counts)
+{
+    extern __shared__ int hist[];
+    for (int e = threadIdx.x; e < E; e += kGroupThreads)
+        hist[e] = 0;
+    __syncthreads();
+    const long long base = (long long)blockIdx.x * (PER * kGroupThreads);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const long long t = base + i * kGroupThreads + threadIdx.x;
+        const int id = t < n ? ids[t] : -1;
+        if ((unsigned)id < (unsigned)E)
+            atomicAdd(&hist[id], 1);              // integers: any order gives the same counts
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kGroupThreads)
+        counts[(size_t)blockIdx.x * E + e] = hist[e];
+}
+
+// nblk = 1: counts unused. LDS: E ints (starts), then 16*E uint16 (per-wavefront counts).
+template <int PER>
+__global__ void __launch_bounds__(kGroupThreads)
+moe_group_place_kernel(const int32_t* ids, int n, int E, int bits, int nblk, const int32_t* counts, int32_t* order,
+                       int32_t* position, int32_t* offsets)
+{
+    extern __shared__ int start[];                // E: first place of this block's slots of each expert
+    uint16_t* cnt = reinterpret_cast<uint16_t*>(start + E);    // [16][E]
+    __shared__ int wsum[kGroupWavesN];
+    const int tid = threadIdx.x, lane = tid % kWave, w = tid / kWave;
+    const int blk = blockIdx.x;
+    const long long first = (long long)blk * (PER * kGroupThreads) + (long long)w * (PER * kWave) + lane;
+    int id[PER], rank[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const long long t = first + i * kWave;
+        id[i] = t < n ? ids[t] : -1;
+    }
+    for (int i = tid; i < (kGroupWavesN * E + 1) / 2; i += kGroupThreads)
+        reinterpret_cast<uint32_t*>(cnt)[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const bool ok = (unsigned)id[i] < (unsigned)E;
+        const unsigned long long live = __ballot(ok);
+        const unsigned long long m = same_id(ok ? id[i] : 0, bits, live);
+        rank[i] = 0;
+        if (ok) {
+            const int before = __popcll(m & ((1ull << lane) - 1ull));
+            const int have = cnt[w * E + id[i]];
+            rank[i] = have + before;
+            // one lane per id writes, after every lane of the wavefront has read
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            if (before == 0)
+                cnt[w * E + id[i]] = (uint16_t)(have + __popcll(m));
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+    __syncthreads();
+    // per expert: earlier wavefronts of this block, earlier blocks, all blocks
+    int done = 0;                                 // slots of the experts before this chunk of 1024 experts
+    for (int e0 = 0; e0 < E; e0 += kGroupThreads) {
+        const int e = e0 + tid;
+        int mine = 0, earlier = 0, all = 0;
+        if (e < E) {
+#pragma unroll
+            for (int q = 0; q < kGroupWavesN; ++q) {
+                const int c = cnt[q * E + e];
+                cnt[q * E + e] = (uint16_t)mine;
+                mine += c;
+            }
+            if (nblk == 1) {
+                all = mine;
+            } else {
+                for (int q = 0; q < nblk; ++q) {
+                    const int c = counts[(size_t)q * E + e];
+                    earlier += q < blk ? c : 0;
+                    all += c;
+                }
+            }
+        }
+        int total = 0;
+        const int at = done + block_exclusive(all, wsum, total);
+        if (e < E) {
+            start[e] = at + earlier;
+            if (blk == 0)
+                offsets[e] = at;
+        }
+        done += total;
+    }
+    if (blk == 0 && tid == 0)
+        offsets[E] = done;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const long long t = first + i * kWave;
+        if (t >= n)
+            continue;
+        int at = -1;
+        if ((unsigned)id[i] < (unsigned)E) {
+            at = start[id[i]] + cnt[w * E + id[i]] + rank[i];
+            order[at] = (int32_t)t;
+        }
+        position[t] = at;
+        if (t >= done)
+            order[t] = -1;                        // places behind the last expert's slots
+    }
+}
+
+size_t group_workspace(int n, int E)
+{
+    if (n <= kGroupOneBlock)
+        return 0;
+    const size_t per = n <= (1 << 18) ? 2 : 8;
+    return ((size_t)n + per * kGroupThreads - 1) / (per * kGroupThreads) * (size_t)E * 4u;
+}
+
+template <int PER>
+static hipError_t launch_place(const int32_t* ids, int n, int E, int nblk, int32_t* counts, int32_t* order,
+                               int32_t* position, int32_t* offsets, hipStream_t s)
+{
+    int bits = 0;
+    while ((1 << bits) < E)
+        ++bits;
+    const size_t lds = (size_t)E * 4 + ((size_t)kGroupWavesN * E + 1) / 2 * 4;
+    const void* f = reinterpret_cast<const void*>(&moe_group_place_kernel<PER>);
+    if (lds > 65536)
+        if (hipError_t e = set_max_dynamic_lds(f, (int)lds))
+            return e;
+    if (nblk > 1) {
+        hipLaunchKernelGGL((moe_group_count_kernel<PER>), dim3((unsigned)nblk), dim3(kGroupThreads), (size_t)E * 4, s, ids,
+                           n, E, counts);
+        if (hipError_t e = hipGetLastError())
+            return e;
+    }
+    hipLaunchKernelGGL((moe_group_place_kernel<PER>), dim3((unsigned)nblk), dim3(kGroupThreads), lds, s, ids, n, E, bits,
+                       nblk, counts, order, position, offsets);
+    return hipGetLastError();
+}
+
+hipError_t launch_group(const int32_t* ids, int n, int E, int32_t* counts, int32_t* order, int32_t* position,
+                        int32_t* offsets, hipStream_t s)
+{
+    if (n <= kGroupThreads)
+        return launch_place<1>(ids, n, E, 1, counts, order, position, offsets, s);
+    if (n <= kGroupOneBlock)
+        return launch_place<8>(ids, n, E, 1, counts, order, position, offsets, s);
+    if (n <= (1 << 18))
+        return launch_place<2>(ids, n, E, (n + 2 * kGroupThreads - 1) / (2 * kGroupThreads), counts, order, position,
+                               offsets, s);
+    return launch_place<8>(ids, n, E, (int)(((long long)n + 8 * kGroupThreads - 1) / (8 * kGroupThreads)), counts, order,
+                           position, offsets, s);
+}
+
+}  // namespace moed
