@@ -157,7 +157,7 @@ struct ProductArgs {
 };
 hipError_t launch_product(const ProductArgs& p, hipStream_t s);
 hipError_t launch_product_few(const ProductArgs& p, int row_tiles, hipStream_t s);
-hipError_t launch_product_tiled(const ProductArgs& p, hipStream_t s);
+hipError_t launch_product_tiled(const ProductArgs& p, int avg_rows, hipStream_t s);
 // Opt-in input check (check.hip). Pointers not used by a step may be null:
 // the gate/up step passes no down matrix and the down step no gate/up ones.
 struct CheckArgs {

@@ -259,6 +259,8 @@ hipError_t launch_product(const ProductArgs& p, hipStream_t s)
 {
     const int experts = p.R < p.E ? p.R : p.E;
     const long long avg = ((long long)p.R + experts - 1) / experts;
+    if (avg > 32)
+        return launch_product_tiled(p, (int)avg, s);
     return launch_product_few(p, avg <= 16 ? 1 : avg <= 32 ? 2 : 4, s);
 }
 
