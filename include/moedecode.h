@@ -378,21 +378,29 @@ int moe_group(const int32_t *topk_ids, int B, int k, int E, int32_t *order,
  *   w_q, w_s [E][N][K] codes ([E][N][K/2] for MOED_MXFP4), [E][N][K/32] scales
  *   out      [R][N] out_rows (gate_up: any moed_rows; matmul: BF16 or F32)
  *   out_s    [R][N/32] for MOED_ROWS_MXFP8 (the rule of moe_norm), else NULL
+ *   workspace at least moe_grouped_workspace_bytes(E, K, N, n_a, a_rows,
+ *            matrices) bytes (matrices: 2 for gate_up, 1 for matmul), 16-byte
+ *            aligned, for the scales in rows of a multiple of 16 bytes; NULL
+ *            where that is 0 (K >= 512, a multiple of 128)
  * Rows from offsets[E] on stay as they were. out may not overlap a. Limits
- * (MOED_ERR_SHAPE): K and N positive multiples of 32, below 2^20; E <= 2048;
- * R and n_a below 2^28; k >= 1. a, out and the code pointers are 16-byte
- * aligned (MOED_ERR_ALIGN). R = 0 launches nothing.
+ * (MOED_ERR_SHAPE): K and N positive multiples of 32, below 2^20, K*N below
+ * 2^32; E <= 2048; R and n_a below 2^28; with an order, `a` below 4 GiB;
+ * k >= 1. a, out and the code pointers are 16-byte aligned, scales 4-byte
+ * (MOED_ERR_ALIGN). R = 0 launches nothing.
  */
 int moe_grouped_gate_up(const void *a, const uint8_t *a_s, int a_rows, int n_a,
                         const int32_t *order, int k, const int32_t *offsets,
                         const uint8_t *wg_q, const uint8_t *wg_s,
                         const uint8_t *wu_q, const uint8_t *wu_s, int weight_format,
                         void *out, uint8_t *out_s, int out_rows,
-                        int R, int E, int K, int N, void *stream);
+                        int R, int E, int K, int N,
+                        void *workspace, size_t workspace_bytes, void *stream);
 int moe_grouped_matmul(const void *a, const uint8_t *a_s, int a_rows, int n_a,
                        const int32_t *order, int k, const int32_t *offsets,
                        const uint8_t *w_q, const uint8_t *w_s, int weight_format,
-                       void *out, int out_rows, int R, int E, int K, int N, void *stream);
+                       void *out, int out_rows, int R, int E, int K, int N,
+                       void *workspace, size_t workspace_bytes, void *stream);
+size_t moe_grouped_workspace_bytes(int E, int K, int N, int n_a, int a_rows, int matrices);
 
 /*
  * out[b][h] = sum_j topk_w[b][j] * y[position[b][j]][h], j in increasing order

@@ -152,12 +152,18 @@ struct ProductArgs {
     void* out;              // [R][N] bf16, f32 or E4M3 codes
     uint8_t* out_s;         // [R][N/32] (MXFP8 out)
     int n_a, k, R, E, K, N;
+    uint32_t inv_k;         // 2^32 / k (2^32 - 1 for k = 1)
+    int s_row;              // bytes between rows of scales: a multiple of 4, at least 16
     bool fp4;               // weights are MXFP4
     int out_kind;           // kOutBF16, kOutF32 or kOutMX8
 };
-hipError_t launch_product(const ProductArgs& p, hipStream_t s);
-hipError_t launch_product_few(const ProductArgs& p, int row_tiles, hipStream_t s);
-hipError_t launch_product_tiled(const ProductArgs& p, int avg_rows, hipStream_t s);
+// The kernels fetch block scales 16 bytes of a row at a time, from dword
+// addresses. Where rows of K/32 bytes are shorter or no multiple of 4, they are
+// first copied to `scales` with rows of a multiple of 16 (product_scales_bytes;
+// 0: not needed).
+size_t product_scales_bytes(int E, int K, int N, int n_a, bool mx_rows, bool two);
+hipError_t launch_product(ProductArgs p, void* scales, hipStream_t s);
+hipError_t launch_product_tiled(const ProductArgs& p, int shape, hipStream_t s);
 // Opt-in input check (check.hip). Pointers not used by a step may be null:
 // the gate/up step passes no down matrix and the down step no gate/up ones.
 struct CheckArgs {

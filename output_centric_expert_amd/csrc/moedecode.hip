@@ -22,6 +22,7 @@ thread_local int g_last_hip = 0;
 constexpr uint32_t kTuningMagic = 0x6D6F6564u;   // "moed": marks an initialised moed_tuning
 
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+inline bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
 inline bool dtype_ok(int d) { return d == MOED_BF16 || d == MOED_F32; }
 
@@ -269,9 +270,24 @@ int check_product(int a_rows, int wfmt, int n_a, int k, bool ordered, int R, int
         return MOED_ERR_SHAPE;
     if (K < 32 || N < 32 || K % 32 != 0 || N % 32 != 0 || K >= kMaxRowLength || N >= kMaxRowLength)
         return MOED_ERR_SHAPE;
+    // the kernels address one expert's matrix, and gathered rows, with 32-bit offsets
+    if ((long long)K * N >= (1LL << 32) || (ordered && (long long)n_a * K * (a_rows == MOED_ROWS_BF16 ? 2 : 1) >= (1LL << 32)))
+        return MOED_ERR_SHAPE;
     if ((a_rows != MOED_ROWS_BF16 && a_rows != MOED_ROWS_MXFP8) || !wformat_ok(wfmt))
         return MOED_ERR_DTYPE;
     return MOED_OK;
+}
+
+// Workspace of a product call, where its scales need one.
+int check_scales(size_t need, const void* workspace, size_t bytes)
+{
+    if (need == 0)
+        return MOED_OK;
+    if (!workspace)
+        return MOED_ERR_NULL;
+    if (bytes < need)
+        return MOED_ERR_WORKSPACE;
+    return aligned16(workspace) ? MOED_OK : MOED_ERR_ALIGN;
 }
 
 moed::ProductArgs product_args(const void* a, const uint8_t* a_s, int n_a, const int32_t* order, int k,
@@ -286,6 +302,7 @@ moed::ProductArgs product_args(const void* a, const uint8_t* a_s, int n_a, const
     p.w_q = w_q; p.w_s = w_s; p.u_q = u_q; p.u_s = u_s;
     p.out = out; p.out_s = out_s;
     p.n_a = n_a; p.k = k; p.R = R; p.E = E; p.K = K; p.N = N;
+    p.inv_k = (uint32_t)(k == 1 ? 0xFFFFFFFFu : (1ull << 32) / (unsigned)k);
     p.fp4 = wfmt == MOED_MXFP4;
     p.out_kind = out_rows;
     return p;
@@ -303,7 +320,7 @@ moed::CombineArgs combine_args(const void* y, int R, const int32_t* position, co
 
 // Workspace of moe_prefill: byte offsets of its parts, each 256-byte aligned.
 struct PrefillLayout {
-    size_t counts, order, position, offsets, a, a_s, y, bytes;
+    size_t counts, order, position, offsets, scales, a, a_s, y, bytes;
 };
 
 int prefill_layout(int B, int E, int k, int H, int I, int x_rows, int out_dtype, PrefillLayout* l)
@@ -314,6 +331,9 @@ int prefill_layout(int B, int E, int k, int H, int I, int x_rows, int out_dtype,
         return MOED_ERR_SHAPE;
     if ((x_rows != MOED_ROWS_BF16 && x_rows != MOED_ROWS_MXFP8) || !dtype_ok(out_dtype))
         return MOED_ERR_DTYPE;
+    const bool mx = x_rows == MOED_ROWS_MXFP8;
+    if ((long long)H * I >= (1LL << 32) || (long long)B * H * (mx ? 1 : 2) >= (1LL << 32))
+        return MOED_ERR_SHAPE;
     const size_t R = (size_t)B * (size_t)k;
     size_t at = 0;
     auto part = [&at](size_t bytes) {
@@ -325,8 +345,11 @@ int prefill_layout(int B, int E, int k, int H, int I, int x_rows, int out_dtype,
     l->order = part(R * 4);
     l->position = part(R * 4);
     l->offsets = part(((size_t)E + 1) * 4);
-    l->a = part(R * (size_t)I * (x_rows == MOED_ROWS_MXFP8 ? 1 : 2));
-    l->a_s = part(x_rows == MOED_ROWS_MXFP8 ? R * (size_t)I / 32 : 0);
+    const size_t up = moed::product_scales_bytes(E, H, I, B, mx, true);
+    const size_t down = moed::product_scales_bytes(E, I, H, (int)R, mx, false);
+    l->scales = part(up > down ? up : down);                  // one product at a time
+    l->a = part(R * (size_t)I * (mx ? 1 : 2));
+    l->a_s = part(mx ? R * (size_t)I / 32 : 0);
     l->y = part(R * (size_t)H * (out_dtype == MOED_F32 ? 4 : 2));
     l->bytes = at;
     return MOED_OK;
@@ -550,10 +573,17 @@ int moe_group(const int32_t* topk_ids, int B, int k, int E, int32_t* order, int3
                                          static_cast<hipStream_t>(stream)));
 }
 
+size_t moe_grouped_workspace_bytes(int E, int K, int N, int n_a, int a_rows, int matrices)
+{
+    if (check_product(a_rows, MOED_MXFP8, n_a, 1, true, 0, E, K, N) || (matrices != 1 && matrices != 2))
+        return 0;
+    return moed::product_scales_bytes(E, K, N, n_a, a_rows == MOED_ROWS_MXFP8, matrices == 2);
+}
+
 int moe_grouped_gate_up(const void* a, const uint8_t* a_s, int a_rows, int n_a, const int32_t* order, int k,
                         const int32_t* offsets, const uint8_t* wg_q, const uint8_t* wg_s, const uint8_t* wu_q,
                         const uint8_t* wu_s, int weight_format, void* out, uint8_t* out_s, int out_rows, int R, int E,
-                        int K, int N, void* stream)
+                        int K, int N, void* workspace, size_t workspace_bytes, void* stream)
 {
     if (out_rows != MOED_ROWS_BF16 && out_rows != MOED_ROWS_F32 && out_rows != MOED_ROWS_MXFP8)
         return MOED_ERR_DTYPE;
@@ -564,16 +594,19 @@ int moe_grouped_gate_up(const void* a, const uint8_t* a_s, int a_rows, int n_a, 
     if (!a || !offsets || !wg_q || !wg_s || !wu_q || !wu_s || !out || (a_rows == MOED_ROWS_MXFP8) != (a_s != nullptr) ||
         (out_rows == MOED_ROWS_MXFP8) != (out_s != nullptr))
         return MOED_ERR_NULL;
-    if (!aligned16(a) || !aligned16(wg_q) || !aligned16(wu_q) || !aligned16(out))
+    if (!aligned16(a) || !aligned16(wg_q) || !aligned16(wu_q) || !aligned16(out) || !aligned4(wg_s) || !aligned4(wu_s) ||
+        !aligned4(a_s))
         return MOED_ERR_ALIGN;
+    if (int st = check_scales(moed::product_scales_bytes(E, K, N, n_a, a_s != nullptr, true), workspace, workspace_bytes))
+        return st;
     return hip_status(moed::launch_product(product_args(a, a_s, n_a, order, k, offsets, wg_q, wg_s, wu_q, wu_s,
                                                         weight_format, out, out_s, out_rows, R, E, K, N),
-                                           static_cast<hipStream_t>(stream)));
+                                           workspace, static_cast<hipStream_t>(stream)));
 }
 
 int moe_grouped_matmul(const void* a, const uint8_t* a_s, int a_rows, int n_a, const int32_t* order, int k,
                        const int32_t* offsets, const uint8_t* w_q, const uint8_t* w_s, int weight_format, void* out,
-                       int out_rows, int R, int E, int K, int N, void* stream)
+                       int out_rows, int R, int E, int K, int N, void* workspace, size_t workspace_bytes, void* stream)
 {
     if (out_rows != MOED_ROWS_BF16 && out_rows != MOED_ROWS_F32)
         return MOED_ERR_DTYPE;
@@ -583,11 +616,13 @@ int moe_grouped_matmul(const void* a, const uint8_t* a_s, int a_rows, int n_a, c
         return MOED_OK;
     if (!a || !offsets || !w_q || !w_s || !out || (a_rows == MOED_ROWS_MXFP8) != (a_s != nullptr))
         return MOED_ERR_NULL;
-    if (!aligned16(a) || !aligned16(w_q) || !aligned16(out))
+    if (!aligned16(a) || !aligned16(w_q) || !aligned16(out) || !aligned4(w_s) || !aligned4(a_s))
         return MOED_ERR_ALIGN;
+    if (int st = check_scales(moed::product_scales_bytes(E, K, N, n_a, a_s != nullptr, false), workspace, workspace_bytes))
+        return st;
     return hip_status(moed::launch_product(product_args(a, a_s, n_a, order, k, offsets, w_q, w_s, nullptr, nullptr,
                                                         weight_format, out, nullptr, out_rows, R, E, K, N),
-                                           static_cast<hipStream_t>(stream)));
+                                           workspace, static_cast<hipStream_t>(stream)));
 }
 
 int moe_combine(const void* y, int y_dtype, int R, const int32_t* position, const float* topk_w, void* out,
@@ -633,7 +668,7 @@ int moe_prefill(const void* x, const uint8_t* x_s, int x_rows, const int32_t* to
     if (workspace_bytes < l.bytes)
         return MOED_ERR_WORKSPACE;
     if (!aligned16(x) || !aligned16(wg_q) || !aligned16(wu_q) || !aligned16(wd_q) || !aligned16(out) ||
-        !aligned16(workspace))
+        !aligned16(workspace) || !aligned4(x_s) || !aligned4(wg_s) || !aligned4(wu_s) || !aligned4(wd_s))
         return MOED_ERR_ALIGN;
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (check_enabled()) {
@@ -653,12 +688,12 @@ int moe_prefill(const void* x, const uint8_t* x_s, int x_rows, const int32_t* to
     if (int st = hip_status(moed::launch_product(
             product_args(x, x_s, B, order, k, offsets, wg_q, wg_s, wu_q, wu_s, weight_format, ws + l.a,
                          mx ? ws + l.a_s : nullptr, x_rows, R, E, H, I),
-            s)))
+            ws + l.scales, s)))
         return st;
     if (int st = hip_status(moed::launch_product(
             product_args(ws + l.a, mx ? ws + l.a_s : nullptr, R, nullptr, 1, offsets, wd_q, wd_s, nullptr, nullptr,
                          weight_format, ws + l.y, nullptr, out_dtype, R, E, I, H),
-            s)))
+            ws + l.scales, s)))
         return st;
     return hip_status(moed::launch_combine(combine_args(ws + l.y, R, position, topk_w, out, out_dtype, B, k, H),
                                            out_dtype == MOED_BF16, s));

@@ -23,41 +23,45 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kProductMaxE = 2048;
 
-// Row tiles of all experts, built by every workgroup in its LDS: first[e] =
-// tiles of the experts before e, lo[e] = first row, n[e] = rows. Offsets are
-// clamped into [0, R], so garbage in them leads to wrong rows but to no access
-// outside, and the total is capped at what any valid offsets can give. All
-// threads must call it; ends with a barrier.
-struct TileList {
-    int* first;             // E + 1
-    int* lo;                // E
-    int* n;                 // E
-};
-
-inline size_t tile_list_bytes(int E) { return ((size_t)3 * E + 1) * 4; }
-
-__device__ __forceinline__ TileList tile_list(int* lds, int E)
-{
-    return TileList{lds, lds + E + 1, lds + 2 * E + 1};
-}
-
+// first[e] = row tiles of the experts before e and begin[e] = first row of e
+// (E + 1 ints of LDS each), built by every workgroup. Offsets are clamped into
+// [0, R] and made to rise, so garbage in them leads to wrong rows but to no
+// access outside. Returns all tiles. All threads must call it; ends with a
+// barrier.
 template <int THREADS>
-__device__ __forceinline__ int build_tiles(const TileList& t, const int32_t* offsets, int E, int R, int tile_rows,
+__device__ __forceinline__ int build_tiles(int* first, int* begin, const int32_t* offsets, int E, int R, int tile_rows,
                                            int* wsum)
 {
     constexpr int W = THREADS / kWave;
     const int tid = threadIdx.x, lane = tid % kWave, w = tid / kWave;
-    int done = 0;
+    int done = 0, top = 0;                                    // tiles and largest offset so far
+    for (int e0 = 0; e0 <= E; e0 += THREADS) {                // begin[e] = the largest of offsets[0..e], clamped
+        const int e = e0 + tid;
+        int lo = e <= E ? offsets[e] : 0;
+        lo = lo < 0 ? 0 : lo > R ? R : lo;
+#pragma unroll
+        for (int d = 1; d < kWave; d <<= 1) {
+            const int o = __shfl_up(lo, d);
+            lo = lane >= d && o > lo ? o : lo;
+        }
+        if (lane == kWave - 1)
+            wsum[w] = lo;
+        __syncthreads();
+        int all = top;
+        lo = top > lo ? top : lo;
+#pragma unroll
+        for (int q = 0; q < W; ++q) {
+            lo = q < w && wsum[q] > lo ? wsum[q] : lo;
+            all = wsum[q] > all ? wsum[q] : all;
+        }
+        if (e <= E)
+            begin[e] = lo;
+        top = all;
+        __syncthreads();
+    }
     for (int e0 = 0; e0 < E; e0 += THREADS) {
         const int e = e0 + tid;
-        int lo = 0, hi = 0;
-        if (e < E) {
-            lo = offsets[e];
-            hi = offsets[e + 1];
-            lo = lo < 0 ? 0 : lo > R ? R : lo;
-            hi = hi < lo ? lo : hi > R ? R : hi;
-        }
-        const int tiles = (hi - lo + tile_rows - 1) / tile_rows;
+        const int tiles = e < E ? (begin[e + 1] - begin[e] + tile_rows - 1) / tile_rows : 0;
         int inc = tiles;
 #pragma unroll
         for (int d = 1; d < kWave; d <<= 1) {
@@ -74,28 +78,24 @@ __device__ __forceinline__ int build_tiles(const TileList& t, const int32_t* off
             before += q < w ? wsum[q] : 0;
             all += wsum[q];
         }
-        if (e < E) {
-            t.first[e] = before + inc - tiles;
-            t.lo[e] = lo;
-            t.n[e] = hi - lo;
-        }
+        if (e < E)
+            first[e] = before + inc - tiles;
         done += all;
         __syncthreads();
     }
     if (tid == 0)
-        t.first[E] = done;
+        first[E] = done;
     __syncthreads();
-    const int most = R / tile_rows + (R < E ? R : E);
-    return done < 0 ? 0 : done < most ? done : most;
+    return done;
 }
 
 // Expert of a global tile: the number of experts whose tiles all come before it.
-__device__ __forceinline__ int tile_expert(const TileList& t, int E, int tile)
+__device__ __forceinline__ int tile_expert(const int* first, int E, int tile)
 {
     const int lane = threadIdx.x % kWave;
     int e = 0;
     for (int base = 0; base < E; base += kWave) {
-        const unsigned long long m = __ballot(base + lane < E && t.first[base + lane + 1] <= tile);
+        const unsigned long long m = __ballot(base + lane < E && first[base + lane + 1] <= tile);
         e += __popcll(m);
         if (m != ~0ull)
             break;
@@ -103,59 +103,94 @@ __device__ __forceinline__ int tile_expert(const TileList& t, int E, int tile)
     return __builtin_amdgcn_readfirstlane(e);
 }
 
-// Source row in `a` of sorted row r; -1 where order[r] lies outside.
-__device__ __forceinline__ int source_row(const ProductArgs& p, int r)
+// Slot of sorted row r (r itself without an order), and the row of `a` that a
+// slot reads: slot / k, -1 where that lies outside.
+__device__ __forceinline__ int slot_of(const ProductArgs& p, int r)
 {
-    if (!p.order)
-        return r;
-    const int t = p.order[r];
-    const int s = t < 0 ? -1 : t / p.k;
-    return s < p.n_a ? s : -1;
+    return p.order ? p.order[r] : r;
 }
 
-// Stores NF fragments of 4 consecutive outputs of row r: fragment f holds
-// outputs n0 + 16f + 4g .. +3 (g = lane / 16). For MXFP8 the fragments 2f and
-// 2f+1 of the four lane groups are one block. All 64 lanes must call it.
-template <int OUT, int NF>
-__device__ __forceinline__ void store_row(const ProductArgs& p, int r, int n0, int g, bool valid, f32x4 (&y)[NF])
+__device__ __forceinline__ int source_row(const ProductArgs& p, int slot)
 {
-    const size_t at = (size_t)r * (size_t)p.N + (size_t)(n0 + 4 * g);
+    if (!p.order)
+        return slot;
+    // slot / k by the reciprocal 2^32 / k, off by at most one
+    int q = (int)__umulhi((unsigned)slot, p.inv_k);
+    const int rest = slot - q * p.k;
+    q += rest >= p.k ? 1 : rest < 0 ? -1 : 0;
+    return slot < 0 || q >= p.n_a ? -1 : q;
+}
+
+// Largest of v over the four lane groups (lanes with equal lane % 16).
+__device__ __forceinline__ uint32_t max_over_groups(uint32_t v)
+{
+    const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = a[0] > a[1] ? a[0] : a[1];
+    const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return b[0] > b[1] ? b[0] : b[1];
+}
+
+// Stores 16 rows (m .. m+15 of the expert whose rows begin at row0) of NF
+// fragments: lane (col, g) holds outputs n + 16f + 4g .. +3 of row m + col in
+// o[f]. They go through `mine` (LDS of this wavefront alone, rows of `stride`
+// bytes), so that neighbouring lanes store neighbouring 16-byte pieces of a row
+// and lines are written whole. For MXFP8 the fragments 2f and 2f+1 are a block.
+template <int OUT, int NF>
+__device__ __forceinline__ void store_tile_rows(const ProductArgs& p, uint8_t* mine, int stride, int row0, int m, int rows,
+                                                int n, f32x4 (&o)[NF])
+{
+    constexpr int kBytes = OUT == kOutBF16 ? 2 : 1;
+    constexpr int kPieces = NF * kBytes;                      // 16-byte pieces of a row
+    const int lane = threadIdx.x % kWave, g = lane / 16, col = lane % 16;
+    uint8_t* at = mine + col * stride;
+    if constexpr (OUT == kOutF32) {                           // 16 bytes a lane as they are
+        if (m + col < rows) {
+            float* out = static_cast<float*>(p.out) + (size_t)(row0 + m + col) * (size_t)p.N + (size_t)(n + 4 * g);
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+                if (n + 16 * f < p.N)
+                    *reinterpret_cast<f32x4*>(out + 16 * f) = o[f];
+        }
+        return;
+    }
     if constexpr (OUT == kOutMX8) {
+        static_assert(NF % 2 == 0, "whole blocks");
 #pragma unroll
         for (int f = 0; f < NF; f += 2) {
-            uint32_t m = 0;
+            uint32_t a = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t a = __float_as_uint(y[f][i]) & 0x7FFFFFFFu;
-                const uint32_t b = __float_as_uint(y[f + 1][i]) & 0x7FFFFFFFu;
-                m = a > m ? a : m;
-                m = b > m ? b : m;
+                const uint32_t u = __float_as_uint(o[f][i]) & 0x7FFFFFFFu, v = __float_as_uint(o[f + 1][i]) & 0x7FFFFFFFu;
+                a = u > a ? u : a;
+                a = v > a ? v : a;
             }
-            const uint32_t o = (uint32_t)__shfl_xor((int)m, 16);
-            m = o > m ? o : m;
-            const uint32_t q = (uint32_t)__shfl_xor((int)m, 32);
-            m = q > m ? q : m;
-            const uint32_t c = mx8_scale_code(m);
-            if (valid && n0 + 16 * f < p.N) {
-                uint8_t* out = static_cast<uint8_t*>(p.out) + at + 16 * f;
-                *reinterpret_cast<uint32_t*>(out) = mx8_codes4(y[f][0], y[f][1], y[f][2], y[f][3], c);
-                *reinterpret_cast<uint32_t*>(out + 16) = mx8_codes4(y[f + 1][0], y[f + 1][1], y[f + 1][2], y[f + 1][3], c);
-                if (g == 0)
-                    p.out_s[((size_t)r * (size_t)p.N + (size_t)n0) / 32 + f / 2] = (uint8_t)c;
-            }
+            a = max_over_groups(a);
+            const uint32_t c = mx8_scale_code(a);
+            *reinterpret_cast<uint32_t*>(at + 16 * f + 4 * g) = mx8_codes4(o[f][0], o[f][1], o[f][2], o[f][3], c);
+            *reinterpret_cast<uint32_t*>(at + 16 * f + 16 + 4 * g) =
+                mx8_codes4(o[f + 1][0], o[f + 1][1], o[f + 1][2], o[f + 1][3], c);
+            if (g == 0 && m + col < rows && n + 16 * f < p.N)
+                p.out_s[((size_t)(row0 + m + col) * (size_t)p.N + (size_t)n) / 32 + f / 2] = (uint8_t)c;
         }
     } else {
 #pragma unroll
         for (int f = 0; f < NF; ++f) {
-            if (valid && n0 + 16 * f < p.N) {
-                if constexpr (OUT == kOutBF16)
-                    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p.out) + at + 16 * f) =
-                        u32x2{f32x2_to_bf16x2_rne(y[f][0], y[f][1]), f32x2_to_bf16x2_rne(y[f][2], y[f][3])};
-                else
-                    *reinterpret_cast<f32x4*>(static_cast<float*>(p.out) + at + 16 * f) = y[f];
-            }
+            uint32_t* q = reinterpret_cast<uint32_t*>(at + (16 * f + 4 * g) * 2);
+            q[0] = f32x2_to_bf16x2_rne(o[f][0], o[f][1]);
+            q[1] = f32x2_to_bf16x2_rne(o[f][2], o[f][3]);
         }
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int i = 0; i < (16 * kPieces + kWave - 1) / kWave; ++i) {
+        const int piece = i * kWave + lane, r = piece / kPieces, c = piece % kPieces;
+        if (r < 16 && m + r < rows && n + c * (16 / kBytes) < p.N) {
+            const u32x4 v = *reinterpret_cast<const u32x4*>(mine + r * stride + 16 * c);
+            uint8_t* out = static_cast<uint8_t*>(p.out) + ((size_t)(row0 + m + r) * (size_t)p.N + (size_t)n) * kBytes + 16 * c;
+            *reinterpret_cast<u32x4*>(out) = v;
+        }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 }
 
 }  // namespace moed

@@ -18,273 +18,420 @@ __device__ const u32x4 kZeros = {0, 0, 0, 0};     // source of the values behind
 // waits on vmcnt before a barrier. Written as asm because the compiler makes
 // every later LDS read wait for the builtin's load, whatever buffer it fills.
 // (m0 is set by each; nothing else in these kernels uses it.)
-__device__ __forceinline__ void load_to_lds16(const void* src, uint32_t base)
+// The address is a uniform base plus a lane's 32-bit offset.
+__device__ __forceinline__ void load_to_lds16(const uint8_t* from, uint32_t offset, uint32_t base)
 {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(base) : "memory");
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(from), "s"(base) : "memory");
 }
 
-__device__ __forceinline__ void load_to_lds4(const void* src, uint32_t base)
+// The same from an address of each lane's own.
+__device__ __forceinline__ void load_to_lds16(const uint8_t* from, uint32_t base)
 {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(base) : "memory");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(base) : "memory");
 }
 
-template <int ROWS, bool FP4, int RT, int NT, int WR, int WN>
+template <int ROWS, bool FP4, int OUT, int RT, int NT, int WR, int WN>
 struct Shape {
     static constexpr bool kMX = ROWS == kRowsMX;
-    static constexpr int kThreads = WR * WN * kWave;
+    static constexpr int kWaves = WR * WN, kThreads = kWaves * kWave;
     static constexpr int kBM = 16 * RT * WR;                  // rows of a tile
     static constexpr int kBN = 16 * NT * WN;                  // weight rows of a tile
-    static constexpr int kBK = kMX ? 128 : 64;                // values of a step
-    static constexpr int kRU = ROWS == kRowsMXExact ? 4 : 8;  // 16-byte units of a row and step
-    static constexpr int kWU = kBK / (FP4 ? 32 : 16);         // ... of a weight row and step
-    static constexpr int kRowLoads = kBM * kRU / kThreads;
-    static constexpr int kWLoads = kBN * kWU / kThreads;
+    static constexpr int kBK = 128;                           // values of a step
+    static constexpr int kRU = ROWS == kRowsBF16 ? 16 : 8;    // 16-byte units of a row and step
+    static constexpr int kWU = FP4 ? 4 : 8;                   // ... of a weight row and step
+    static constexpr int kRowLoads = (kBM * kRU + kThreads - 1) / kThreads;
+    static constexpr int kWLoads = (kBN * kWU + kThreads - 1) / kThreads;
     static constexpr int kRowBytes = kBM * kRU * 16, kWBytes = kBN * kWU * 16;
-    static constexpr int kBufBytes = kRowBytes + kWBytes;
-    // block scales of 128 values: one dword per row and weight row
-    static constexpr int kScaleRows = kBN + (ROWS != kRowsBF16 ? kBM : 0);
+    static constexpr int kWAt = 2 * kRowBytes;
+    // block scales: of every weight row, and of every row in MXFP8
+    static constexpr int kScaleRows = (kBN + (ROWS != kRowsBF16 ? kBM : 0) + kWave - 1) / kWave * kWave;
     static constexpr int kScaleLoads = (kScaleRows + kThreads - 1) / kThreads;
-    static constexpr int kScaleBytes = kScaleLoads * kThreads * 4;
-    static constexpr int kLds = 2 * kBufBytes + 2 * kScaleBytes;
-    static_assert(kBM * kRU % kThreads == 0 && kBN * kWU % kThreads == 0, "whole loads per thread");
+    static constexpr int kScaleBytes = kScaleRows * 16;
+    // 16 rows of a wavefront's outputs on their way out
+    static constexpr int kOutBytes = OUT == kOutBF16 ? 2 : OUT == kOutF32 ? 4 : 1;
+    static constexpr int kScaleAt = kWAt + 2 * kWBytes;
+    static constexpr int kEnd = kScaleAt + 2 * kScaleBytes;
+    static constexpr int scratch_row(int out_frags) { return OUT == kOutF32 ? 0 : out_frags * 16 * kOutBytes + 16; }
+    // it lies in the second row buffer, which is free between a tile's last and the next one's second step
+    static constexpr bool inside(int out_frags) { return kWaves * 16 * scratch_row(out_frags) <= kRowBytes; }
+    static constexpr int scratch_at(int out_frags) { return inside(out_frags) ? kRowBytes : kEnd; }
+    static constexpr int bad_at(int out_frags) { return kEnd + (inside(out_frags) ? 0 : kWaves * 16 * scratch_row(out_frags)); }
+    static constexpr int lds(int out_frags) { return bad_at(out_frags) + 2 * kBM; }
+    static_assert(kBM * kRU % kWave == 0 && kBN * kWU % kWave == 0, "whole loads per wavefront");
     static_assert((kThreads / kRU) % 8 == 0 && (kThreads / kWU) % 8 == 0, "a thread's loads share their place in the row");
+    // loads of a step's weights by the wavefront that has the fewest
+    static constexpr int kWeightLoads = kBN * kWU / kThreads;
 };
 
+template <int N>
+__device__ __forceinline__ void wait_loads()
+{
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
 // Units of a row are stored at c ^ swizzle(row), so that the lanes that read one
-// unit of 8 (or 16) neighbouring rows together meet different banks.
+// unit of 8 neighbouring rows together meet different banks.
 template <int UNITS>
 __device__ __forceinline__ int swizzle(int row)
 {
-    return UNITS == 8 ? row & 7 : UNITS == 4 ? (row >> 1) & 3 : (row >> 2) & 1;
+    return UNITS >= 8 ? row & 7 : (row >> 1) & 3;
 }
+
+// Byte offset of unit c of row `col` (below 16) of a fragment; the same unit of
+// fragment f lies f * 16 * UNITS * 16 bytes on.
+template <int UNITS>
+__device__ __forceinline__ int unit_at(int col, int c)
+{
+    return (col * UNITS + (c ^ swizzle<UNITS>(col))) * 16;
+}
+
+__device__ __forceinline__ u32x4 lds16(const uint8_t* p) { return *reinterpret_cast<const u32x4*>(p); }
+
+// One tile: rows m0 .. of expert e, outputs n0 .. .
+struct Tile {
+    int e, m0, n0, rows, row0;
+    bool live;
+};
 
 }  // namespace
 
 template <int ROWS, bool FP4, bool GLU, int OUT, int RT, int NT, int WR, int WN>
 __global__ void __launch_bounds__(WR * WN * kWave)
-moe_product_tiled_kernel(ProductArgs p, int nblk, int group_blocks, int aligned_scales)
+moe_product_tiled_kernel(ProductArgs p, int nblk, int group_blocks)
 {
-    using S = Shape<ROWS, FP4, RT, NT, WR, WN>;
-    constexpr bool kMX = S::kMX;
+    using S = Shape<ROWS, FP4, OUT, RT, NT, WR, WN>;
     constexpr int kOutFrags = GLU ? NT / 2 : NT;
     constexpr int kNeurons = 16 * kOutFrags * WN;             // outputs of a tile
+    constexpr int kScratchRow = S::scratch_row(kOutFrags);
+    constexpr int kAhead = 1;
     extern __shared__ __align__(16) uint8_t lds[];
-    uint32_t* const scales = reinterpret_cast<uint32_t*>(lds + 2 * S::kBufBytes);   // [2][kScaleBytes / 4]
-    const TileList tl = tile_list(reinterpret_cast<int*>(lds + S::kLds), p.E);
-    __shared__ int wsum[WR * WN];
+    uint8_t* const bad = lds + S::bad_at(kOutFrags);          // [2][kBM]: rows without a source
+    int* const first = reinterpret_cast<int*>(lds + S::lds(kOutFrags));           // tiles before each expert
+    int* const begin = first + p.E + 1;                       // its first row
+    __shared__ int wsum[S::kWaves];
     const int tid = threadIdx.x, lane = tid % kWave;
     const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int g = lane / 16, col = lane % 16;
     const int wr = w / WN, wn = w % WN;
-    const int tiles = build_tiles<S::kThreads>(tl, p.offsets, p.E, p.R, S::kBM, wsum);
+    const int tiles = build_tiles<S::kThreads>(first, begin, p.offsets, p.E, p.R, S::kBM, wsum);
     const long long items = (long long)tiles * nblk;
-    const int steps = (p.K + S::kBK - 1) / S::kBK;
-    const size_t w_row = FP4 ? (size_t)p.K / 2 : (size_t)p.K, s_row = (size_t)p.K / 32;
+    const size_t w_row = FP4 ? (size_t)p.K / 2 : (size_t)p.K, s_row = (size_t)p.s_row;
     const size_t a_row = ROWS == kRowsBF16 ? 2 * (size_t)p.K : (size_t)p.K;
     const uint32_t lds0 = (uint32_t)(size_t)(__attribute__((address_space(3))) uint8_t*)lds;
 
-    for (long long item = xcd_contiguous(blockIdx.x, gridDim.x); item < items; item += gridDim.x) {
-        // items of one expert are neighbours; within it blocks of weight rows in
-        // groups, so that a group's weights and the expert's rows meet in one L2
-        const int e = tile_expert(tl, p.E, (int)(item / nblk));
+    // items of one expert are neighbours; within it blocks of weight rows in
+    // groups, so that a group's weights and the expert's rows meet in one L2
+    auto find = [&](long long item) {
+        Tile t;
+        t.live = false;
+        t.e = t.m0 = t.n0 = t.rows = t.row0 = 0;
+        if (item >= items)
+            return t;
+        const int e = tile_expert(first, p.E, (int)(item / nblk));
         if (e >= p.E)
-            continue;                                         // uniform
-        const int mt = tl.first[e + 1] - tl.first[e];
-        const long long local = item - (long long)tl.first[e] * nblk;
+            return t;
+        const int mt = first[e + 1] - first[e];
+        const long long local = item - (long long)first[e] * nblk;
         const int grp = (int)(local / ((long long)group_blocks * mt));
         const int rest = (int)(local - (long long)grp * group_blocks * mt);
         const int in_grp = nblk - grp * group_blocks < group_blocks ? nblk - grp * group_blocks : group_blocks;
-        const int n0 = (grp * group_blocks + rest % in_grp) * kNeurons;
-        const int m0 = (rest / in_grp) * S::kBM;
-        const int rows = tl.n[e], row0 = tl.lo[e];
-        if (m0 < 0 || m0 >= rows || n0 >= p.N)
-            continue;                                         // only for offsets that decrease
+        t.e = __builtin_amdgcn_readfirstlane(e);
+        t.n0 = __builtin_amdgcn_readfirstlane((grp * group_blocks + rest % in_grp) * kNeurons);
+        t.m0 = __builtin_amdgcn_readfirstlane((rest / in_grp) * S::kBM);
+        t.row0 = __builtin_amdgcn_readfirstlane(begin[t.e]);
+        t.rows = __builtin_amdgcn_readfirstlane(begin[t.e + 1]) - t.row0;
+        t.live = t.m0 >= 0 && t.m0 < t.rows && t.n0 >= 0 && t.n0 < p.N;   // false only for offsets that decrease
+        return t;
+    };
+    const int rc = (tid % S::kRU) ^ swizzle<S::kRU>(tid / S::kRU);        // this thread's unit within a row and step
+    const int wc = (tid % S::kWU) ^ swizzle<S::kWU>(tid / S::kWU);
+    auto tile_row = [&](const Tile& t, int r) {                           // rows behind the last repeat it
+        return t.row0 + (t.m0 + r < t.rows ? t.m0 + r : t.rows - 1);
+    };
+    // slots of a tile: of this thread's row loads, and of its row's scales
+    auto sources = [&](const Tile& t, int (&src)[S::kRowLoads + 1]) {
+#pragma unroll
+        for (int i = 0; i < S::kRowLoads; ++i)
+            src[i] = slot_of(p, tile_row(t, i * (S::kThreads / S::kRU) + tid / S::kRU));
+        src[S::kRowLoads] = 0;
+        if constexpr (ROWS != kRowsBF16) {
+            const int rr = (S::kScaleLoads - 1) * S::kThreads + tid;      // BN is a multiple of the threads, or below them
+            static_assert(S::kScaleLoads <= 2 && (S::kScaleLoads == 1 || S::kBN % S::kThreads == 0), "one row per thread");
+            if (rr >= S::kBN && rr < S::kScaleRows)
+                src[S::kRowLoads] = slot_of(p, tile_row(t, rr - S::kBN));
+        }
+    };
 
-        // sources of this thread's loads (rows behind the last repeat it)
-        const uint8_t* rsrc[S::kRowLoads];
-        const uint8_t* wsrc[S::kWLoads];
-        const int rc = (tid % S::kRU) ^ swizzle<S::kRU>(tid / S::kRU);      // unit within the row and step
-        const int wc = (tid % S::kWU) ^ swizzle<S::kWU>(tid / S::kWU);
+    // Sources: uniform bases and 32-bit offsets (a wavefront's load of weights
+    // lies within one fragment, so its matrix is uniform too); addresses for the
+    // scales.
+    const uint8_t *rbase = nullptr, *wbase = nullptr, *ubase = nullptr;
+    uint32_t roff[S::kRowLoads], woff[S::kWLoads];
+    const uint8_t* ssrc[S::kScaleLoads];
+    auto is_up = [&](int place) { return GLU && place / 16 % NT >= NT / 2; };       // place: weight row of the tile
+    auto weight_row = [&](const Tile& t, int place) {                               // row of its expert's matrix
+        const int f = place / 16 % NT;
+        const int n = t.n0 + (place / (16 * NT) * kOutFrags + (GLU && f >= NT / 2 ? f - NT / 2 : f)) * 16 + place % 16;
+        return (uint32_t)(n < p.N ? n : p.N - 1);
+    };
+    auto point = [&](const Tile& t, const int (&src)[S::kRowLoads + 1], int parity) {
+        rbase = static_cast<const uint8_t*>(p.a) + (p.order ? 0 : (size_t)(t.row0 + t.m0) * a_row);
+        const size_t m = (size_t)t.e * (size_t)p.N;
+        wbase = p.w_q + m * w_row;
+        if constexpr (GLU)
+            ubase = p.u_q + m * w_row;
+        auto row_of = [&](int slot) {                         // rows behind rbase
+            return p.order ? source_row(p, slot) : slot - (t.row0 + t.m0);
+        };
 #pragma unroll
         for (int i = 0; i < S::kRowLoads; ++i) {
-            int r = m0 + i * (S::kThreads / S::kRU) + tid / S::kRU;
-            r = r < rows ? r : rows - 1;
-            const int src = source_row(p, row0 + r);
-            rsrc[i] = static_cast<const uint8_t*>(p.a) + (size_t)(src < 0 ? 0 : src) * a_row + 16 * rc;
+            const int from = row_of(src[i]);
+            roff[i] = (uint32_t)(from < 0 ? 0 : from) * (uint32_t)a_row + 16u * rc;
+            const int r = i * (S::kThreads / S::kRU) + tid / S::kRU;
+            if (tid % S::kRU == 0 && r < S::kBM)
+                bad[parity * S::kBM + r] = from < 0;
         }
-        auto weight_row = [&](int rr, bool& up) {             // weight row of place rr of the tile
-            const int wv = rr / (16 * NT), f = rr / 16 % NT;
-            up = GLU && f >= NT / 2;
-            const int n = n0 + (wv * kOutFrags + (up ? f - NT / 2 : f)) * 16 + rr % 16;
-            return (size_t)e * (size_t)p.N + (size_t)(n < p.N ? n : p.N - 1);
-        };
 #pragma unroll
-        for (int i = 0; i < S::kWLoads; ++i) {
-            bool up;
-            const size_t n = weight_row(i * (S::kThreads / S::kWU) + tid / S::kWU, up);
-            wsrc[i] = (up ? p.u_q : p.w_q) + n * w_row + 16 * wc;
-        }
-        const uint8_t* ssrc[S::kScaleLoads];
+        for (int i = 0; i < S::kWLoads; ++i)
+            woff[i] = weight_row(t, i * (S::kThreads / S::kWU) + tid / S::kWU) * (uint32_t)w_row + 16u * wc;
 #pragma unroll
         for (int i = 0; i < S::kScaleLoads; ++i) {
-            const int rr = i * S::kThreads + tid;
-            if (rr < S::kBN) {
-                bool up;
-                const size_t n = weight_row(rr, up);
-                ssrc[i] = (up ? p.u_s : p.w_s) + n * s_row;
+            const int place = i * S::kThreads + tid;
+            if (ROWS != kRowsBF16 && place >= S::kBN) {
+                const int from = p.order ? source_row(p, src[S::kRowLoads]) : src[S::kRowLoads];
+                ssrc[i] = p.a_s + (size_t)(from < 0 ? 0 : from) * s_row;
             } else {
-                int r = m0 + (rr - S::kBN);
-                r = r < rows ? r : rows - 1;
-                const int src = ROWS != kRowsBF16 ? source_row(p, row0 + r) : 0;
-                ssrc[i] = (ROWS != kRowsBF16 ? p.a_s : p.w_s) + (size_t)(src < 0 ? 0 : src) * s_row;
+                const int at = place < S::kBN ? place : 0;
+                ssrc[i] = (is_up(at) ? p.u_s : p.w_s) + (m + weight_row(t, at)) * s_row;
             }
         }
+    };
+    const uint8_t* const zeros = reinterpret_cast<const uint8_t*>(&kZeros);
+    const int full = p.K / S::kBK, steps = (p.K + S::kBK - 1) / S::kBK;
+    auto stage_rows = [&](int st) {
+        const uint32_t to = lds0 + (uint32_t)(st & 1) * S::kRowBytes + (uint32_t)w * 1024u;
+        const uint8_t* from = rbase + (size_t)st * (S::kRU * 16);
+        if (st < full) {
+#pragma unroll
+            for (int i = 0; i < S::kRowLoads; ++i)
+                if (S::kBM * S::kRU % S::kThreads == 0 || i * S::kThreads + w * kWave < S::kBM * S::kRU)
+                    load_to_lds16(from, roff[i], to + i * S::kThreads * 16);
+        } else {                                              // a K that is no multiple of 128: zeros behind its end
+            const bool in = st * S::kBK + rc * (S::kBK / S::kRU) < p.K;
+#pragma unroll
+            for (int i = 0; i < S::kRowLoads; ++i)
+                if (S::kBM * S::kRU % S::kThreads == 0 || i * S::kThreads + w * kWave < S::kBM * S::kRU)
+                    load_to_lds16(in ? from + roff[i] : zeros, to + i * S::kThreads * 16);
+        }
+    };
+    auto stage_weights = [&](int st) {
+        const uint32_t to = lds0 + S::kWAt + (uint32_t)(st & 1) * S::kWBytes + (uint32_t)w * 1024u;
+        const bool in = st < full || st * S::kBK + wc * (S::kBK / S::kWU) < p.K;
+#pragma unroll
+        for (int i = 0; i < S::kWLoads; ++i) {
+            if (S::kBN * S::kWU % S::kThreads != 0 && i * S::kThreads + w * kWave >= S::kBN * S::kWU)
+                continue;                                     // whole wavefronts
+            const uint8_t* from = (is_up(i * (S::kThreads / S::kWU) + w * (kWave / S::kWU)) ? ubase : wbase) +
+                                  (size_t)st * (S::kWU * 16);
+            if (st < full)
+                load_to_lds16(from, woff[i], to + i * S::kThreads * 16);
+            else
+                load_to_lds16(in ? from + woff[i] : zeros, to + i * S::kThreads * 16);
+        }
+    };
+    // Block scales are fetched 16 bytes (four steps) of a row at a time: a load
+    // that takes four bytes of each of 64 rows costs the cache about as much as
+    // one that takes a line of each. Where a row is no multiple of 16, the last
+    // fetch is of the row's last 16 bytes, the wanted ones at its end.
+    auto scales_from = [&](int chunk) { return 16 * chunk + 16 <= p.s_row ? 16 * chunk : p.s_row - 16; };
+    auto stage_scales = [&](int chunk) {
+        const uint32_t to = lds0 + S::kScaleAt + (uint32_t)(chunk & 1) * S::kScaleBytes;
+        const int from = scales_from(chunk);
+#pragma unroll
+        for (int i = 0; i < S::kScaleLoads; ++i) {
+            const int place = i * S::kThreads + w * kWave;    // of this wavefront's first lane
+            if (S::kScaleRows % S::kThreads == 0 || place < S::kScaleRows)
+                load_to_lds16(ssrc[i] + from, to + place * 16);
+        }
+    };
+    // the steps a tile begins with
+    auto stage_first = [&]() {
+        stage_scales(0);
+        stage_rows(0);
+        stage_weights(0);
+        if (steps > 1)
+            stage_weights(1);
+    };
 
-        auto stage = [&](int st) {
-            const uint32_t buf = lds0 + (uint32_t)(st & 1) * S::kBufBytes + (uint32_t)w * 1024u;
-            const int k0 = st * S::kBK;
-            if (k0 + S::kBK <= p.K) {
+    // this lane's places in the buffers
+    const int w0 = wn * NT * 16 * S::kWU * 16, r0 = wr * RT * 16 * S::kRU * 16;
+    constexpr int kWFrag = 16 * S::kWU * 16, kRFrag = 16 * S::kRU * 16;      // bytes of a fragment
+    f32x4 acc[RT][NT];
+    // One step's products . `release` is called once the step's weights and scales are in registers.
+    auto compute = [&](int st, auto release) {
+        const uint8_t* wb = lds + S::kWAt + (st & 1) * S::kWBytes + w0;
+        const uint8_t* rb = lds + (st & 1) * S::kRowBytes + r0;
+        const int chunk = st / 4;
+        const uint8_t* sb = lds + S::kScaleAt + (chunk & 1) * S::kScaleBytes + (4 * st - scales_from(chunk)) + 16 * col + g;
+        const uint8_t* wsb = sb + wn * NT * 256;
+        const uint8_t* rsb = sb + (S::kBN + wr * RT * 16) * 16;
+        if constexpr (S::kMX) {
+            i32x8 wv[NT], av[kAhead + 1];
+            int wsc[NT], asc[RT];
+            const uint8_t* rlo = rb + unit_at<8>(col, g);
+            const uint8_t* rhi = rb + unit_at<8>(col, 4 + g);
+            auto read_a = [&](int r) {
+                const u32x4 lo = lds16(rlo + r * kRFrag), hi = lds16(rhi + r * kRFrag);
+                av[r % (kAhead + 1)] =
+                    i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+            };
+            auto read_w = [&](int f) {
+                const u32x4 lo = lds16(wb + unit_at<S::kWU>(col, g) + f * kWFrag);
+                const u32x4 hi = FP4 ? u32x4{0, 0, 0, 0} : lds16(wb + unit_at<S::kWU>(col, FP4 ? 0 : 4 + g) + f * kWFrag);
+                wv[f] = i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+                wsc[f] = wsb[f * 256];
+            };
 #pragma unroll
-                for (int i = 0; i < S::kRowLoads; ++i)
-                    load_to_lds16(rsrc[i] + (size_t)st * (S::kRU * 16), buf + i * S::kThreads * 16);
+            for (int f = 0; f < NT; ++f)
+                read_w(f);
 #pragma unroll
-                for (int i = 0; i < S::kWLoads; ++i)
-                    load_to_lds16(wsrc[i] + (size_t)st * (S::kWU * 16), buf + S::kRowBytes + i * S::kThreads * 16);
-            } else {                                          // the last step of a K that is no multiple of kBK
-                const bool rin = k0 + rc * (S::kBK / S::kRU) < p.K, win = k0 + wc * (S::kBK / S::kWU) < p.K;
+            for (int r = 0; r < RT; ++r)
+                asc[r] = rsb[r * 256];
 #pragma unroll
-                for (int i = 0; i < S::kRowLoads; ++i)
-                    load_to_lds16(rin ? rsrc[i] + (size_t)st * (S::kRU * 16) : reinterpret_cast<const uint8_t*>(&kZeros),
-                                  buf + i * S::kThreads * 16);
+            for (int r = 0; r < kAhead && r < RT; ++r)
+                read_a(r);
+            release();
+            __builtin_amdgcn_sched_barrier(0);
+            // fragments of rows are read kAhead before their use, so that the reads of one pass under
+            // the matrix instructions of the others
 #pragma unroll
-                for (int i = 0; i < S::kWLoads; ++i)
-                    load_to_lds16(win ? wsrc[i] + (size_t)st * (S::kWU * 16) : reinterpret_cast<const uint8_t*>(&kZeros),
-                                  buf + S::kRowBytes + i * S::kThreads * 16);
+            for (int r = 0; r < RT; ++r) {
+                if (r + kAhead < RT)
+                    read_a(r + kAhead);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int f = 0; f < NT; ++f)
+                    acc[r][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        wv[f], av[r % (kAhead + 1)], acc[r][f], FP4 ? 4 : 0, 0, 0, wsc[f], 0, asc[r]);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            if (kMX || (st & 1) == 0) {                       // scales of 128 values
-                const int q = kMX ? st : st / 2;
-                if (aligned_scales) {
+        } else {
+            // lane group g multiplies the block 32g .. 32g+31 of the step, 8 values per instruction
+            u32x4 wq[NT][FP4 ? 1 : 2];
+            float wsc[NT], asc[ROWS == kRowsMXExact ? RT : 1];
 #pragma unroll
-                    for (int i = 0; i < S::kScaleLoads; ++i)
-                        load_to_lds4(ssrc[i] + 4 * (size_t)q, lds0 + 2 * S::kBufBytes + (q & 1) * S::kScaleBytes +
-                                                                  (uint32_t)(i * S::kThreads + w * kWave) * 4u);
+            for (int f = 0; f < NT; ++f) {
+                if constexpr (FP4) {
+                    wq[f][0] = lds16(wb + unit_at<4>(col, g) + f * kWFrag);
                 } else {
+                    wq[f][0] = lds16(wb + unit_at<8>(col, 2 * g) + f * kWFrag);
+                    wq[f][1] = lds16(wb + unit_at<8>(col, 2 * g + 1) + f * kWFrag);
+                }
+                wsc[f] = ue8m0_to_f32(wsb[f * 256]);
+            }
+            if constexpr (ROWS == kRowsMXExact) {
 #pragma unroll
-                    for (int i = 0; i < S::kScaleLoads; ++i) {
-                        uint32_t v = 0;
+                for (int r = 0; r < RT; ++r)
+                    asc[r] = ue8m0_to_f32(rsb[r * 256]);
+            }
+            release();
 #pragma unroll
-                        for (int b = 0; b < 4; ++b)
-                            if (128 * q + 32 * b < p.K)
-                                v |= (uint32_t)ssrc[i][4 * (size_t)q + b] << (8 * b);
-                        scales[(q & 1) * (S::kScaleBytes / 4) + i * S::kThreads + tid] = v;
+            for (int q = 0; q < 4; ++q) {
+                bf16x8 wv[NT];
+#pragma unroll
+                for (int f = 0; f < NT; ++f) {
+                    if constexpr (FP4) {
+                        wv[f] = decode8_scaled_fp4(wq[f][0][q], wsc[f]);
+                    } else {
+                        const u32x4 c = wq[f][q / 2];
+                        wv[f] = decode8_scaled((q & 1) ? u32x2{c.z, c.w} : u32x2{c.x, c.y}, wsc[f]);
                     }
                 }
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    bf16x8 av;
+                    if constexpr (ROWS == kRowsMXExact) {
+                        const u32x4 c = lds16(rb + unit_at<8>(col, 2 * g + q / 2) + r * kRFrag);
+                        av = decode8_scaled((q & 1) ? u32x2{c.z, c.w} : u32x2{c.x, c.y}, asc[r]);
+                    } else {
+                        av = __builtin_bit_cast(bf16x8, lds16(rb + unit_at<16>(col, 4 * g + q) + r * kRFrag));
+                    }
+#pragma unroll
+                    for (int f = 0; f < NT; ++f)
+                        acc[r][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[f], av, acc[r][f], 0, 0, 0);
+                }
             }
-        };
+        }
+    };
 
-        f32x4 acc[RT][NT];
+    long long item = xcd_contiguous(blockIdx.x, gridDim.x);
+    Tile t = find(item);
+    int parity = 0;
+    if (t.live) {
+        int src[S::kRowLoads + 1];
+        sources(t, src);
+        point(t, src, 0);
+        stage_first();
+    }
+    while (item < items) {
+        Tile next = find(item + gridDim.x);
+        int nsrc[S::kRowLoads + 1];
+        if (next.live)
+            sources(next, nsrc);                              // used after this tile's steps
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
             for (int f = 0; f < NT; ++f)
                 acc[r][f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-        __syncthreads();                                      // the last item's readers of both buffers are done
-        stage(0);
-        for (int st = 0; st < steps; ++st) {
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            __syncthreads();                                  // step st is in LDS; the other buffer is free
-            if (st + 1 < steps)
-                stage(st + 1);
-            const uint8_t* rb = lds + (st & 1) * S::kBufBytes;
-            const uint8_t* wb = rb + S::kRowBytes;
-            const int q = kMX ? st : st / 2;
-            const uint8_t* sb = reinterpret_cast<const uint8_t*>(scales) + (q & 1) * S::kScaleBytes;
-            const int sbyte = kMX ? g : 2 * (st & 1) + g / 2;
-            auto unit = [&](const uint8_t* base, int units, int row, int c) {
-                const int sw = units == 8 ? swizzle<8>(row) : units == 4 ? swizzle<4>(row) : swizzle<2>(row);
-                return *reinterpret_cast<const u32x4*>(base + (row * units + (c ^ sw)) * 16);
-            };
-            if constexpr (kMX) {
-                i32x8 wv[NT];
-                int wsc[NT];
-#pragma unroll
-                for (int f = 0; f < NT; ++f) {
-                    const int row = (wn * NT + f) * 16 + col;
-                    const u32x4 lo = unit(wb, S::kWU, row, g);
-                    const u32x4 hi = FP4 ? u32x4{0, 0, 0, 0} : unit(wb, S::kWU, row, 4 + g);
-                    wv[f] = i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
-                    wsc[f] = sb[row * 4 + sbyte];
-                }
-#pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    const int row = (wr * RT + r) * 16 + col;
-                    const u32x4 lo = unit(rb, 8, row, g), hi = unit(rb, 8, row, 4 + g);
-                    const i32x8 av{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
-                    const int asc = sb[(S::kBN + row) * 4 + sbyte];
-#pragma unroll
-                    for (int f = 0; f < NT; ++f)
-                        acc[r][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv[f], av, acc[r][f], FP4 ? 4 : 0, 0,
-                                                                                     0, wsc[f], 0, asc);
-                }
-            } else {
-                // lane group g multiplies values 16g .. 16g+15 of the step, 8 per matrix instruction
-                bf16x8 wv[NT][2];
-#pragma unroll
-                for (int f = 0; f < NT; ++f) {
-                    const int row = (wn * NT + f) * 16 + col;
-                    const float sc = ue8m0_to_f32(sb[row * 4 + sbyte]);
-                    if constexpr (FP4) {
-                        const u32x2 c = *reinterpret_cast<const u32x2*>(
-                            wb + (row * 2 + ((g / 2) ^ swizzle<2>(row))) * 16 + 8 * (g % 2));
-                        wv[f][0] = decode8_scaled_fp4(c.x, sc);
-                        wv[f][1] = decode8_scaled_fp4(c.y, sc);
-                    } else {
-                        const u32x4 c = unit(wb, 4, row, g);
-                        wv[f][0] = decode8_scaled(u32x2{c.x, c.y}, sc);
-                        wv[f][1] = decode8_scaled(u32x2{c.z, c.w}, sc);
-                    }
-                }
-#pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    const int row = (wr * RT + r) * 16 + col;
-                    bf16x8 av[2];
-                    if constexpr (ROWS == kRowsMXExact) {
-                        const float sc = ue8m0_to_f32(sb[(S::kBN + row) * 4 + sbyte]);
-                        const u32x4 c = unit(rb, 4, row, g);
-                        av[0] = decode8_scaled(u32x2{c.x, c.y}, sc);
-                        av[1] = decode8_scaled(u32x2{c.z, c.w}, sc);
-                    } else {
-                        av[0] = __builtin_bit_cast(bf16x8, unit(rb, 8, row, 2 * g));
-                        av[1] = __builtin_bit_cast(bf16x8, unit(rb, 8, row, 2 * g + 1));
-                    }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int f = 0; f < NT; ++f)
-                            acc[r][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[f][h], av[h], acc[r][f], 0, 0, 0);
-                }
+        if (t.live) {
+            for (int st = 0; st < steps; ++st) {
+                // A step's weights are asked for nearly two steps ahead (they come from far, and their buffer is
+                // free as soon as every wavefront has its fragments), its rows one step ahead. Step st is in LDS
+                // once this wavefront's loads of it, and then everybody's, are done.
+                if (st + 1 < steps)
+                    wait_loads<S::kWeightLoads>();
+                else
+                    wait_loads<0>();
+                __syncthreads();
+                if (st + 1 < steps)
+                    stage_rows(st + 1);
+                compute(st, [&] {
+                    __syncthreads();                          // everybody has the step's weights
+                    if ((st & 3) == 2 && st + 2 < steps)
+                        stage_scales(st / 4 + 1);
+                    if (st + 2 < steps)
+                        stage_weights(st + 2);
+                });
             }
         }
-
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            const int m = m0 + (wr * RT + r) * 16 + col;
-            const bool valid = m < rows;
-            const int at = row0 + (valid ? m : rows - 1);
-            const bool bad = source_row(p, at) < 0;
-            f32x4 o[kOutFrags];
-#pragma unroll
-            for (int f = 0; f < kOutFrags; ++f)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float v = acc[r][f][i];
-                    if constexpr (GLU)
-                        v = swiglu(v, acc[r][f + NT / 2][i]);
-                    o[f][i] = bad ? __builtin_nanf("") : v;
-                }
-            store_row<OUT>(p, at, n0 + wn * kOutFrags * 16, g, valid, o);
+        // the next tile's first steps are on their way while this one is stored
+        __syncthreads();
+        if (next.live) {
+            point(next, nsrc, parity ^ 1);
+            stage_first();
         }
+        if (t.live) {
+            uint8_t* mine = lds + S::scratch_at(kOutFrags) + w * 16 * kScratchRow;
+            const int nw = t.n0 + wn * kOutFrags * 16;        // this wavefront's first output
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                const bool none = bad[parity * S::kBM + (wr * RT + r) * 16 + col];
+                f32x4 o[kOutFrags];
+#pragma unroll
+                for (int f = 0; f < kOutFrags; ++f)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float v = acc[r][f][i];
+                        if constexpr (GLU)
+                            v = swiglu(v, acc[r][f + NT / 2][i]);
+                        o[f][i] = none ? __builtin_nanf("") : v;
+                    }
+                store_tile_rows<OUT, kOutFrags>(p, mine, kScratchRow, t.row0, t.m0 + (wr * RT + r) * 16, t.rows, nw, o);
+            }
+        }
+        item += gridDim.x;
+        t = next;
+        parity ^= 1;
     }
 }
 
@@ -293,73 +440,79 @@ namespace {
 template <int ROWS, bool FP4, bool GLU, int OUT, int RT, int NT, int WR, int WN>
 hipError_t launch_shape(const ProductArgs& p, hipStream_t s)
 {
-    using S = Shape<ROWS, FP4, RT, NT, WR, WN>;
-    constexpr int kNeurons = 16 * (GLU ? NT / 2 : NT) * WN;
-    const size_t lds = S::kLds + tile_list_bytes(p.E);
+    using S = Shape<ROWS, FP4, OUT, RT, NT, WR, WN>;
+    constexpr int kOutFrags = GLU ? NT / 2 : NT;
+    constexpr int kNeurons = 16 * kOutFrags * WN;
+    const size_t lds = S::lds(kOutFrags) + ((size_t)p.E + 1) * 8;
     const void* f = reinterpret_cast<const void*>(&moe_product_tiled_kernel<ROWS, FP4, GLU, OUT, RT, NT, WR, WN>);
     if (lds > 65536)
         if (hipError_t e = set_max_dynamic_lds(f, (int)lds))
             return e;
     const int nblk = (p.N + kNeurons - 1) / kNeurons;
     const long long tiles = (long long)p.R / S::kBM + (p.R < p.E ? p.R : p.E);
-    const int per_cu = (int)((size_t)163840 / lds);
+    const int per_cu = (int)((size_t)163840 / (lds + 64));
     long long grid = tiles * nblk;
     const long long most = 256LL * (per_cu < 1 ? 1 : per_cu > 4 ? 4 : per_cu);
     grid = grid < most ? grid : most;
-    const bool aligned = (p.K / 32) % 4 == 0 && ((uintptr_t)p.w_s & 3) == 0 && (!p.u_s || ((uintptr_t)p.u_s & 3) == 0) &&
-                         (!p.a_s || ((uintptr_t)p.a_s & 3) == 0);
     // weight rows of about 2 MiB per group of blocks
     const long long bytes = (long long)S::kBN * p.K / (FP4 ? 2 : 1);
     long long group = (2LL << 20) / bytes;
     group = group < 1 ? 1 : group > nblk ? nblk : group;
     hipLaunchKernelGGL((moe_product_tiled_kernel<ROWS, FP4, GLU, OUT, RT, NT, WR, WN>), dim3((unsigned)grid),
-                       dim3(S::kThreads), lds, s, p, nblk, (int)group, aligned ? 1 : 0);
+                       dim3(S::kThreads), lds, s, p, nblk, (int)group);
     return hipGetLastError();
 }
 
 template <int ROWS, bool FP4, bool GLU, int OUT>
-hipError_t tiled_shape(const ProductArgs& p, int avg, hipStream_t s)
+hipError_t tiled_shape(const ProductArgs& p, int shape, hipStream_t s)
 {
-    if constexpr (ROWS == kRowsMX) {
-        if (avg >= 256)
-            return launch_shape<ROWS, FP4, GLU, OUT, 8, 4, 2, 4>(p, s);   // 256 x 256
-        return launch_shape<ROWS, FP4, GLU, OUT, 4, 4, 2, 2>(p, s);       // 128 x 128
-    } else {
-        if (avg >= 96)
-            return launch_shape<ROWS, FP4, GLU, OUT, 4, 4, 2, 2>(p, s);   // 128 x 128
-        return launch_shape<ROWS, FP4, GLU, OUT, 4, 4, 1, 4>(p, s);       // 64 x 256
+    constexpr bool M = ROWS == kRowsMX, B = ROWS == kRowsBF16;
+    switch (shape) {
+    case 0: if constexpr (M) return launch_shape<ROWS, FP4, GLU, OUT, 8, 4, 2, 4>(p, s); break;   // 256 x 256
+    case 1: return launch_shape<ROWS, FP4, GLU, OUT, 4, 4, 2, 4>(p, s);       // 128 x 256
+    case 2: return launch_shape<ROWS, FP4, GLU, OUT, 4, 4, 2, 2>(p, s);       // 128 x 128
+    case 3: return launch_shape<ROWS, FP4, GLU, OUT, 4, 4, 1, 4>(p, s);       // 64 x 256
+    case 4: return launch_shape<ROWS, FP4, GLU, OUT, 2, 4, 2, 2>(p, s);       // 64 x 128
+    case 5: return launch_shape<ROWS, FP4, GLU, OUT, 4, 4, 1, 2>(p, s);       // 64 x 128, 2 waves
+    case 6: return launch_shape<ROWS, FP4, GLU, OUT, 2, 4, 1, 4>(p, s);       // 32 x 256
+    case 7: return launch_shape<ROWS, FP4, GLU, OUT, 1, 4, 1, 4>(p, s);       // 16 x 256
+    case 8: return launch_shape<ROWS, FP4, GLU, OUT, 1, 4, 1, 2>(p, s);       // 16 x 128
+    case 9: return launch_shape<ROWS, FP4, GLU, OUT, 2, 4, 1, 2>(p, s);       // 32 x 128
+    case 10: if constexpr (M||B) return launch_shape<ROWS, FP4, GLU, OUT, 8, 4, 1, 4>(p, s); break;       // 128 x 256, 4 waves
+    case 11: if constexpr (M||B) return launch_shape<ROWS, FP4, GLU, OUT, 8, 4, 1, 2>(p, s); break;       // 128 x 128, 2 waves
     }
+    return hipErrorInvalidValue;
 }
 
 template <bool FP4>
-hipError_t tiled_rows(const ProductArgs& p, int avg, hipStream_t s)
+hipError_t tiled_rows(const ProductArgs& p, int shape, hipStream_t s)
 {
     if (p.u_q) {
         if (!p.a_s) {
             if (p.out_kind == kOutBF16)
-                return tiled_shape<kRowsBF16, FP4, true, kOutBF16>(p, avg, s);
+                return tiled_shape<kRowsBF16, FP4, true, kOutBF16>(p, shape, s);
             if (p.out_kind == kOutF32)
-                return tiled_shape<kRowsBF16, FP4, true, kOutF32>(p, avg, s);
-            return tiled_shape<kRowsBF16, FP4, true, kOutMX8>(p, avg, s);
+                return tiled_shape<kRowsBF16, FP4, true, kOutF32>(p, shape, s);
+            return tiled_shape<kRowsBF16, FP4, true, kOutMX8>(p, shape, s);
         }
         if (p.out_kind == kOutBF16)
-            return tiled_shape<kRowsMX, FP4, true, kOutBF16>(p, avg, s);
+            return tiled_shape<kRowsMX, FP4, true, kOutBF16>(p, shape, s);
         if (p.out_kind == kOutF32)
-            return tiled_shape<kRowsMXExact, FP4, true, kOutF32>(p, avg, s);
-        return tiled_shape<kRowsMX, FP4, true, kOutMX8>(p, avg, s);
+            return tiled_shape<kRowsMXExact, FP4, true, kOutF32>(p, shape, s);
+        return tiled_shape<kRowsMX, FP4, true, kOutMX8>(p, shape, s);
     }
     if (!p.a_s)
-        return p.out_kind == kOutBF16 ? tiled_shape<kRowsBF16, FP4, false, kOutBF16>(p, avg, s)
-                                      : tiled_shape<kRowsBF16, FP4, false, kOutF32>(p, avg, s);
-    return p.out_kind == kOutBF16 ? tiled_shape<kRowsMX, FP4, false, kOutBF16>(p, avg, s)
-                                  : tiled_shape<kRowsMXExact, FP4, false, kOutF32>(p, avg, s);
+        return p.out_kind == kOutBF16 ? tiled_shape<kRowsBF16, FP4, false, kOutBF16>(p, shape, s)
+                                      : tiled_shape<kRowsBF16, FP4, false, kOutF32>(p, shape, s);
+    return p.out_kind == kOutBF16 ? tiled_shape<kRowsMX, FP4, false, kOutBF16>(p, shape, s)
+                                  : tiled_shape<kRowsMXExact, FP4, false, kOutF32>(p, shape, s);
 }
 
 }  // namespace
 
-hipError_t launch_product_tiled(const ProductArgs& p, int avg, hipStream_t s)
+hipError_t launch_product_tiled(const ProductArgs& p, int shape, hipStream_t s)
 {
-    return p.fp4 ? tiled_rows<true>(p, avg, s) : tiled_rows<false>(p, avg, s);
+    return p.fp4 ? tiled_rows<true>(p, shape, s) : tiled_rows<false>(p, shape, s);
 }
 
 }  // namespace moed

@@ -27,7 +27,7 @@ EXPORTS = ("moed_workspace_bytes", "moe_decode", "moe_decode_gate_up", "moe_deco
            "moed_selftest_decode", "moed_bench_read", "moed_bench_copy", "moed_status_string",
            "moed_last_hip_error", "moed_tuning_init", "moe_decode_tuned", "moe_decode_gate_up_tuned",
            "moe_decode_down_tuned", "moe_decode_noalloc", "moed_bench_read_cfg", "moe_norm",
-           "moe_group_workspace_bytes", "moe_group", "moe_grouped_gate_up", "moe_grouped_matmul", "moe_combine",
+           "moe_group_workspace_bytes", "moe_group", "moe_grouped_workspace_bytes", "moe_grouped_gate_up", "moe_grouped_matmul", "moe_combine",
            "moe_prefill_workspace_bytes", "moe_prefill")
 
 
@@ -85,9 +85,11 @@ def load() -> ctypes.CDLL:
         lib.moe_group_workspace_bytes.restype = Z
         lib.moe_group.argtypes = [P, I, I, I, P, P, P, P, Z, P]
         lib.moe_group.restype = I
-        lib.moe_grouped_gate_up.argtypes = [P, P, I, I, P, I] + [P] * 5 + [I, P, P, I] + [I] * 4 + [P]
+        lib.moe_grouped_workspace_bytes.argtypes = [I] * 6
+        lib.moe_grouped_workspace_bytes.restype = Z
+        lib.moe_grouped_gate_up.argtypes = [P, P, I, I, P, I] + [P] * 5 + [I, P, P, I] + [I] * 4 + [P, Z, P]
         lib.moe_grouped_gate_up.restype = I
-        lib.moe_grouped_matmul.argtypes = [P, P, I, I, P, I] + [P] * 3 + [I, P, I] + [I] * 4 + [P]
+        lib.moe_grouped_matmul.argtypes = [P, P, I, I, P, I] + [P] * 3 + [I, P, I] + [I] * 4 + [P, Z, P]
         lib.moe_grouped_matmul.restype = I
         lib.moe_combine.argtypes = [P, I, I, P, P, P, I, I, I, I, P]
         lib.moe_combine.restype = I
@@ -308,37 +310,50 @@ def moe_route(logits, k: int, n_shared: int = 0, routed_scale: float = 1.0, ids=
 
 # ---------------------------------------------------------------- the block for prompts
 
-def _arg(t, name, dtypes, shape, device, optional=False):
-    """_ptr with the checks of the prompt-side calls: one of `dtypes`, on `device`."""
-    if t is None:
-        if optional:
-            return None
+def _refuse(t, name, dtypes, shape, dev):
+    """Raise what is wrong with an argument of a prompt-side call."""
+    if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: a tensor is needed")
-    if t.dtype not in (dtypes if isinstance(dtypes, tuple) else (dtypes,)):
+    if t.dtype not in dtypes:
         raise TypeError(f"{name}: unsupported type {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be a GPU tensor")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, the call runs on {device}")
-    return _ptr(t, name, None, shape)
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, the call runs on the current device cuda:{dev}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name}: must be contiguous")
 
 
-def _current(x, name):
-    """The device of a prompt-side call: the current one, which `x` has to be on."""
-    if not isinstance(x, torch.Tensor) or not x.is_cuda:
-        raise ValueError(f"{name}: must be a GPU tensor")
-    here = torch.device("cuda", torch.cuda.current_device())
-    if x.device != here:
-        raise ValueError(f"{name}: on {x.device}, the current device is {here}")
-    return here
+# These calls take microseconds on the GPU, so the checks of an argument are one expression, and what is wrong
+# is found out only when it fails.
+def _arg(t, name, dtypes, shape, dev):
+    """Address of a contiguous tensor of one of `dtypes` and of `shape` (None: any) on device index `dev`."""
+    try:
+        if t.dtype in dtypes and t.get_device() == dev and (shape is None or t.shape == shape) and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, dtypes, shape, dev)
 
 
-def _new(shape, dtype, device, stream):
+def _opt(t, name, dtypes, shape, dev):
+    return None if t is None else _arg(t, name, dtypes, shape, dev)
+
+
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(stream, dev):
+    if stream is None:
+        return _current_raw_stream(dev) if _current_raw_stream else torch.cuda.current_stream(dev).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _new(shape, dtype, x, stream):
     """A tensor made here for a call on `stream`: its memory is not handed out again before that work is done."""
-    t = torch.empty(shape, dtype=dtype, device=device)
+    t = torch.empty(shape, dtype=dtype, device=x.device)
     if stream is not None:
         if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
+            stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=x.device)
         here = torch.cuda.current_stream()
         if stream.cuda_stream != here.cuda_stream:
             # the memory may have been an earlier tensor's of the current stream, whose work comes first
@@ -347,6 +362,7 @@ def _new(shape, dtype, device, stream):
     return t
 
 
+_U8, _I32, _F32, _BF = (torch.uint8,), (torch.int32,), (torch.float32,), (torch.bfloat16,)
 _F = (torch.bfloat16, torch.float32)
 
 
@@ -357,49 +373,49 @@ def moe_norm(x, gain, residual=None, eps: float = 1e-6, out_dtype=torch.bfloat16
     out = RMSNorm(x + residual) * gain in out_dtype (None: no plain output); residual_out = x + residual in the
     residual's type (None without a residual; give the residual itself for an update in place); with
     quantize, out_q uint8 [B, H] and out_s uint8 [B, H/32] are the same values in MXFP8, else None."""
-    dev = _current(x, "x")
+    dev = torch.cuda.current_device()
     if x.dim() != 2:
         raise ValueError("x: expected shape [B, H]")
     B, H = x.shape
     if quantize and H % 32:
         raise ValueError("quantize needs H to be a multiple of 32")
     if out is None and out_dtype is not None:
-        out = _new((B, H), out_dtype, dev, stream)
+        out = _new((B, H), out_dtype, x, stream)
     if residual is not None and residual_out is None:
-        residual_out = _new((B, H), residual.dtype, dev, stream)
+        residual_out = _new((B, H), residual.dtype, x, stream)
     if quantize:
-        out_q = _new((B, H), torch.uint8, dev, stream) if out_q is None else out_q
-        out_s = _new((B, H // 32), torch.uint8, dev, stream) if out_s is None else out_s
+        out_q = _new((B, H), torch.uint8, x, stream) if out_q is None else out_q
+        out_s = _new((B, H // 32), torch.uint8, x, stream) if out_s is None else out_s
     elif out_q is not None or out_s is not None:
         raise ValueError("out_q and out_s need quantize=True")
     st = load().moe_norm(
-        _arg(x, "x", _F, (B, H), dev), _DT[x.dtype], _arg(residual, "residual", _F, (B, H), dev, True),
+        _arg(x, "x", _F, (B, H), dev), _DT[x.dtype], _opt(residual, "residual", _F, (B, H), dev),
         _DT[residual.dtype] if residual is not None else MOED_BF16, _arg(gain, "gain", _F, (H,), dev), _DT[gain.dtype],
-        float(eps), _arg(residual_out, "residual_out", residual.dtype if residual is not None else _F, (B, H), dev, True),
-        _arg(out, "out", _F, (B, H), dev, True), _DT[out.dtype] if out is not None else MOED_BF16,
-        _arg(out_q, "out_q", torch.uint8, (B, H), dev, True), _arg(out_s, "out_s", torch.uint8, (B, H // 32), dev, True),
-        B, H, _stream(stream))
+        float(eps), _opt(residual_out, "residual_out", (residual.dtype,) if residual is not None else _F, (B, H), dev),
+        _opt(out, "out", _F, (B, H), dev), _DT[out.dtype] if out is not None else MOED_BF16,
+        _opt(out_q, "out_q", _U8, (B, H), dev), _opt(out_s, "out_s", _U8, (B, H // 32), dev),
+        B, H, _raw_stream(stream, dev))
     _check(st, "moe_norm")
     return out, residual_out, out_q, out_s
 
 
 def moe_group(topk_ids, E: int, order=None, position=None, offsets=None, workspace=None, stream=None):
     """Routed slots sorted by expert: (order int32 [B*k], position int32 [B, k], offsets int32 [E+1])."""
-    dev = _current(topk_ids, "topk_ids")
+    dev = torch.cuda.current_device()
     if topk_ids.dim() != 2:
         raise ValueError("topk_ids: expected shape [B, k]")
     B, k = topk_ids.shape
-    order = _new((B * k,), torch.int32, dev, stream) if order is None else order
-    position = _new((B, k), torch.int32, dev, stream) if position is None else position
-    offsets = _new((E + 1,), torch.int32, dev, stream) if offsets is None else offsets
+    order = _new((B * k,), torch.int32, topk_ids, stream) if order is None else order
+    position = _new((B, k), torch.int32, topk_ids, stream) if position is None else position
+    offsets = _new((E + 1,), torch.int32, topk_ids, stream) if offsets is None else offsets
     need = int(load().moe_group_workspace_bytes(B, k, E))
     if workspace is None and need:
-        workspace = _new((need,), torch.uint8, dev, stream)
+        workspace = _new((need,), torch.uint8, topk_ids, stream)
     st = load().moe_group(
-        _arg(topk_ids, "topk_ids", torch.int32, (B, k), dev), B, k, E, _arg(order, "order", torch.int32, (B * k,), dev),
-        _arg(position, "position", torch.int32, (B, k), dev), _arg(offsets, "offsets", torch.int32, (E + 1,), dev),
-        _arg(workspace, "workspace", torch.uint8, None, dev, True), workspace.numel() if workspace is not None else 0,
-        _stream(stream))
+        _arg(topk_ids, "topk_ids", _I32, (B, k), dev), B, k, E, _arg(order, "order", _I32, (B * k,), dev),
+        _arg(position, "position", _I32, (B, k), dev), _arg(offsets, "offsets", _I32, (E + 1,), dev),
+        _opt(workspace, "workspace", _U8, None, dev), workspace.numel() if workspace is not None else 0,
+        _raw_stream(stream, dev))
     _check(st, "moe_group")
     return order, position, offsets
 
@@ -409,9 +425,9 @@ def _rows(a, a_s, name, dev):
     if a.dim() != 2:
         raise ValueError(f"{name}: expected shape [rows, K]")
     if a_s is None:
-        return _arg(a, name, torch.bfloat16, None, dev), None, MOED_ROWS_BF16
-    return (_arg(a, name, torch.uint8, None, dev),
-            _arg(a_s, f"{name}_s", torch.uint8, (a.shape[0], a.shape[1] // 32), dev), MOED_ROWS_MXFP8)
+        return _arg(a, name, _BF, None, dev), None, MOED_ROWS_BF16
+    return (_arg(a, name, _U8, None, dev),
+            _arg(a_s, f"{name}_s", _U8, (a.shape[0], a.shape[1] // 32), dev), MOED_ROWS_MXFP8)
 
 
 def _product_shape(a, offsets, w_q, order):
@@ -421,65 +437,81 @@ def _product_shape(a, offsets, w_q, order):
     return (order.shape[0] if order is not None else a.shape[0]), E, N, a.shape[1]
 
 
+def moe_grouped_workspace_bytes(E: int, K: int, N: int, n_a: int, quantized: bool = False, matrices: int = 1) -> int:
+    """Workspace of moe_grouped_matmul (matrices 1) or moe_grouped_gate_up (2): 0 where K is a multiple of 128, 512 at least."""
+    return int(load().moe_grouped_workspace_bytes(E, K, N, n_a, MOED_ROWS_MXFP8 if quantized else MOED_ROWS_BF16, matrices))
+
+
+def _product_workspace(workspace, E, K, N, n_a, a_rows, matrices, x, dev, stream):
+    need = int(load().moe_grouped_workspace_bytes(E, K, N, n_a, a_rows, matrices))
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = _new((need,), torch.uint8, x, stream)
+    return _arg(workspace, "workspace", _U8, None, dev), workspace.numel(), workspace
+
+
 def moe_grouped_gate_up(a, offsets, wg_q, wg_s, wu_q, wu_s, order=None, k: int = 1, a_s=None, out_dtype=torch.bfloat16,
-                        quantize: bool = False, out=None, out_s=None, stream=None, wformat="mxfp8"):
+                        quantize: bool = False, out=None, out_s=None, workspace=None, stream=None, wformat="mxfp8"):
     """SiLU(Wg a) * (Wu a) over the sorted rows of each expert: returns out [R, N] in out_dtype, or with
     quantize (codes uint8 [R, N], scales uint8 [R, N/32]) in MXFP8.
 
     a: bfloat16 [n, K], or MXFP8 codes uint8 [n, K] with a_s uint8 [n, K/32]. Row r reads a[order[r] // k]
     (order None: a[r]) and belongs to the expert e with offsets[e] <= r < offsets[e+1]; rows from offsets[E] on
     stay as they were."""
-    dev = _current(a, "a")
+    dev = torch.cuda.current_device()
     ap, asp, a_rows = _rows(a, a_s, "a", dev)
     R, E, N, K = _product_shape(a, offsets, wg_q, order)
     KB = _kb(K, wformat)
     if quantize:
-        out = _new((R, N), torch.uint8, dev, stream) if out is None else out
-        out_s = _new((R, N // 32), torch.uint8, dev, stream) if out_s is None else out_s
+        out = _new((R, N), torch.uint8, a, stream) if out is None else out
+        out_s = _new((R, N // 32), torch.uint8, a, stream) if out_s is None else out_s
     elif out is None:
-        out = _new((R, N), out_dtype, dev, stream)
+        out = _new((R, N), out_dtype, a, stream)
+    wp, wb, workspace = _product_workspace(workspace, E, K, N, a.shape[0], a_rows, 2, a, dev, stream)
     st = load().moe_grouped_gate_up(
-        ap, asp, a_rows, a.shape[0], _arg(order, "order", torch.int32, (R,), dev, True), k,
-        _arg(offsets, "offsets", torch.int32, (E + 1,), dev),
-        _arg(wg_q, "wg_q", torch.uint8, (E, N, KB), dev), _arg(wg_s, "wg_s", torch.uint8, (E, N, K // 32), dev),
-        _arg(wu_q, "wu_q", torch.uint8, (E, N, KB), dev), _arg(wu_s, "wu_s", torch.uint8, (E, N, K // 32), dev),
-        _WF[wformat], _arg(out, "out", torch.uint8 if quantize else _F, (R, N), dev),
-        _arg(out_s, "out_s", torch.uint8, (R, N // 32), dev, not quantize),
-        MOED_ROWS_MXFP8 if quantize else _DT[out.dtype], R, E, K, N, _stream(stream))
+        ap, asp, a_rows, a.shape[0], _opt(order, "order", _I32, (R,), dev), k,
+        _arg(offsets, "offsets", _I32, (E + 1,), dev),
+        _arg(wg_q, "wg_q", _U8, (E, N, KB), dev), _arg(wg_s, "wg_s", _U8, (E, N, K // 32), dev),
+        _arg(wu_q, "wu_q", _U8, (E, N, KB), dev), _arg(wu_s, "wu_s", _U8, (E, N, K // 32), dev),
+        _WF[wformat], _arg(out, "out", _U8 if quantize else _F, (R, N), dev),
+        _arg(out_s, "out_s", _U8, (R, N // 32), dev) if quantize else None,
+        MOED_ROWS_MXFP8 if quantize else _DT[out.dtype], R, E, K, N, wp, wb, _raw_stream(stream, dev))
     _check(st, "moe_grouped_gate_up")
     return (out, out_s) if quantize else out
 
 
 def moe_grouped_matmul(a, offsets, w_q, w_s, order=None, k: int = 1, a_s=None, out_dtype=torch.bfloat16, out=None,
-                       stream=None, wformat="mxfp8"):
+                       workspace=None, stream=None, wformat="mxfp8"):
     """W a over the sorted rows of each expert: returns out [R, N] (rows as in moe_grouped_gate_up)."""
-    dev = _current(a, "a")
+    dev = torch.cuda.current_device()
     ap, asp, a_rows = _rows(a, a_s, "a", dev)
     R, E, N, K = _product_shape(a, offsets, w_q, order)
     if out is None:
-        out = _new((R, N), out_dtype, dev, stream)
+        out = _new((R, N), out_dtype, a, stream)
+    wp, wb, workspace = _product_workspace(workspace, E, K, N, a.shape[0], a_rows, 1, a, dev, stream)
     st = load().moe_grouped_matmul(
-        ap, asp, a_rows, a.shape[0], _arg(order, "order", torch.int32, (R,), dev, True), k,
-        _arg(offsets, "offsets", torch.int32, (E + 1,), dev),
-        _arg(w_q, "w_q", torch.uint8, (E, N, _kb(K, wformat)), dev), _arg(w_s, "w_s", torch.uint8, (E, N, K // 32), dev),
-        _WF[wformat], _arg(out, "out", _F, (R, N), dev), _DT[out.dtype], R, E, K, N, _stream(stream))
+        ap, asp, a_rows, a.shape[0], _opt(order, "order", _I32, (R,), dev), k,
+        _arg(offsets, "offsets", _I32, (E + 1,), dev),
+        _arg(w_q, "w_q", _U8, (E, N, _kb(K, wformat)), dev), _arg(w_s, "w_s", _U8, (E, N, K // 32), dev),
+        _WF[wformat], _arg(out, "out", _F, (R, N), dev), _DT[out.dtype], R, E, K, N, wp, wb, _raw_stream(stream, dev))
     _check(st, "moe_grouped_matmul")
     return out
 
 
 def moe_combine(y, position, topk_w, out=None, out_dtype=torch.bfloat16, stream=None):
     """out[b] = sum_j topk_w[b, j] * y[position[b, j]]: returns out [B, H]."""
-    dev = _current(y, "y")
+    dev = torch.cuda.current_device()
     if y.dim() != 2 or position.dim() != 2:
         raise ValueError("expected y [R, H] and position [B, k]")
     R, H = y.shape
     B, k = position.shape
     if out is None:
-        out = _new((B, H), out_dtype, dev, stream)
+        out = _new((B, H), out_dtype, y, stream)
     st = load().moe_combine(
-        _arg(y, "y", _F, (R, H), dev), _DT[y.dtype], R, _arg(position, "position", torch.int32, (B, k), dev),
-        _arg(topk_w, "topk_w", torch.float32, (B, k), dev), _arg(out, "out", _F, (B, H), dev), _DT[out.dtype], B, k, H,
-        _stream(stream))
+        _arg(y, "y", _F, (R, H), dev), _DT[y.dtype], R, _arg(position, "position", _I32, (B, k), dev),
+        _arg(topk_w, "topk_w", _F32, (B, k), dev), _arg(out, "out", _F, (B, H), dev), _DT[out.dtype], B, k, H,
+        _raw_stream(stream, dev))
     _check(st, "moe_combine")
     return out
 
@@ -495,25 +527,25 @@ def moe_prefill(x, topk_ids, topk_w, wg_q, wg_s, wu_q, wu_s, wd_q, wd_s, x_s=Non
                 out_dtype=torch.bfloat16, workspace=None, stream=None, wformat="mxfp8"):
     """The whole layer for prompts: returns out [B, H]. x: bfloat16 [B, H], or MXFP8 codes uint8 with x_s
     uint8 [B, H/32] (moe_norm's quantized output). Same layer as moe_decode, by the grouped products."""
-    dev = _current(x, "x")
+    dev = torch.cuda.current_device()
     xp, xsp, x_rows = _rows(x, x_s, "x", dev)
     B, H = x.shape
     k = topk_ids.shape[1]
     E, I = wg_q.shape[0], wg_q.shape[1]
     HB, IB = _kb(H, wformat), _kb(I, wformat)
     if out is None:
-        out = _new((B, H), out_dtype, dev, stream)
+        out = _new((B, H), out_dtype, x, stream)
     need = moe_prefill_workspace_bytes(B, E, k, H, I, x_s is not None, out.dtype)
     if workspace is None:
-        workspace = _new((max(need, 16),), torch.uint8, dev, stream)
+        workspace = _new((max(need, 16),), torch.uint8, x, stream)
     st = load().moe_prefill(
-        xp, xsp, x_rows, _arg(topk_ids, "topk_ids", torch.int32, (B, k), dev),
-        _arg(topk_w, "topk_w", torch.float32, (B, k), dev),
-        _arg(wg_q, "wg_q", torch.uint8, (E, I, HB), dev), _arg(wg_s, "wg_s", torch.uint8, (E, I, H // 32), dev),
-        _arg(wu_q, "wu_q", torch.uint8, (E, I, HB), dev), _arg(wu_s, "wu_s", torch.uint8, (E, I, H // 32), dev),
-        _arg(wd_q, "wd_q", torch.uint8, (E, H, IB), dev), _arg(wd_s, "wd_s", torch.uint8, (E, H, I // 32), dev),
+        xp, xsp, x_rows, _arg(topk_ids, "topk_ids", _I32, (B, k), dev),
+        _arg(topk_w, "topk_w", _F32, (B, k), dev),
+        _arg(wg_q, "wg_q", _U8, (E, I, HB), dev), _arg(wg_s, "wg_s", _U8, (E, I, H // 32), dev),
+        _arg(wu_q, "wu_q", _U8, (E, I, HB), dev), _arg(wu_s, "wu_s", _U8, (E, I, H // 32), dev),
+        _arg(wd_q, "wd_q", _U8, (E, H, IB), dev), _arg(wd_s, "wd_s", _U8, (E, H, I // 32), dev),
         _WF[wformat], _arg(out, "out", _F, (B, H), dev), _DT[out.dtype], B, E, k, H, I,
-        _arg(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _stream(stream))
+        _arg(workspace, "workspace", _U8, None, dev), workspace.numel(), _raw_stream(stream, dev))
     _check(st, "moe_prefill")
     return out
 

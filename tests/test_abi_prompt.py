@@ -48,21 +48,21 @@ def test_group_rejects(lib):  # noqa: F811
 
 
 def gate_up(lib, a=A, a_s=None, rows=0, n_a=8, order=A, k=2, off=A, wq=A, ws=A, uq=A, us=A, wf=0, out=A, out_s=None,
-            out_rows=0, R=16, E=8, K=64, N=64):
+            out_rows=0, R=16, E=8, K=512, N=64, wsp=None, wsb=0):
     return lib.moe_grouped_gate_up(a, a_s, rows, n_a, order, k, off, wq, ws, uq, us, wf, out, out_s, out_rows, R, E, K, N,
-                                   None)
+                                   wsp, wsb, None)
 
 
-def matmul(lib, a=A, a_s=None, rows=0, n_a=8, order=A, k=2, off=A, wq=A, ws=A, wf=0, out=A, out_rows=0, R=16, E=8, K=64,
-           N=64):
-    return lib.moe_grouped_matmul(a, a_s, rows, n_a, order, k, off, wq, ws, wf, out, out_rows, R, E, K, N, None)
+def matmul(lib, a=A, a_s=None, rows=0, n_a=8, order=A, k=2, off=A, wq=A, ws=A, wf=0, out=A, out_rows=0, R=16, E=8, K=512,
+           N=64, wsp=None, wsb=0):
+    return lib.moe_grouped_matmul(a, a_s, rows, n_a, order, k, off, wq, ws, wf, out, out_rows, R, E, K, N, wsp, wsb, None)
 
 
 @pytest.mark.parametrize("call", [gate_up, matmul])
 def test_products_reject(lib, call):  # noqa: F811
     assert call(lib, R=0) == md.MOED_OK
     for kw in ({"R": -1}, {"R": 1 << 28}, {"n_a": -1}, {"n_a": 0}, {"k": 0}, {"E": 0}, {"E": 2049}, {"K": 48}, {"N": 40},
-               {"K": 0}, {"N": 1 << 20}, {"order": None}):
+               {"K": 0}, {"N": 1 << 20}, {"order": None}, {"K": 1 << 16, "N": 1 << 16}, {"n_a": 1 << 22}):
         assert call(lib, **kw) == md.MOED_ERR_SHAPE, kw
     for kw in ({"rows": 1}, {"rows": 3}, {"wf": 2}, {"out_rows": 3}, {"out_rows": -1}):
         assert call(lib, **kw) == md.MOED_ERR_DTYPE, kw
@@ -70,9 +70,21 @@ def test_products_reject(lib, call):  # noqa: F811
         assert call(lib, **kw) == md.MOED_ERR_NULL, kw
     for name in ("a", "wq", "out"):
         assert call(lib, **{name: MIS}) == md.MOED_ERR_ALIGN, name
+    odd = ctypes.c_void_p(4098)
+    assert call(lib, ws=odd) == md.MOED_ERR_ALIGN
+    assert call(lib, rows=2, a_s=odd) == md.MOED_ERR_ALIGN
+    # K = 64: two scales a row, in rows of 16 in the workspace
+    need = lib.moe_grouped_workspace_bytes(8, 64, 64, 8, 0, 2 if call is gate_up else 1)
+    assert need == 8 * 64 * (2 if call is gate_up else 1) * 16
+    assert call(lib, K=64) == md.MOED_ERR_NULL
+    assert call(lib, K=64, wsp=A, wsb=need - 1) == md.MOED_ERR_WORKSPACE
+    assert call(lib, K=64, wsp=MIS, wsb=need) == md.MOED_ERR_ALIGN
 
 
 def test_products_reject_more(lib):  # noqa: F811
+    assert lib.moe_grouped_workspace_bytes(8, 64, 32, 5, 2, 1) == (8 * 32 + 5) * 16
+    for args in ((8, 512, 32, 5, 2, 1), (8, 768, 32, 5, 0, 2), (8, 48, 32, 5, 0, 2), (8, 64, 32, 5, 0, 3)):
+        assert lib.moe_grouped_workspace_bytes(*args) == 0
     assert matmul(lib, out_rows=2) == md.MOED_ERR_DTYPE
     assert gate_up(lib, out_rows=2) == md.MOED_ERR_NULL                  # codes without scales
     assert gate_up(lib, out_s=A) == md.MOED_ERR_NULL                     # scales without codes
@@ -115,8 +127,11 @@ def test_prefill_rejects(lib):  # noqa: F811
         assert prefill(lib, **{name: MIS}) == md.MOED_ERR_ALIGN, name
     need = lib.moe_prefill_workspace_bytes(2, 8, 2, 64, 32, 0, 0)
     assert prefill(lib, wsb=need - 1) == md.MOED_ERR_WORKSPACE
-    # order, position, offsets, bfloat16 intermediate, bfloat16 rows, each rounded up to 256 bytes
-    assert need == 256 + 256 + 256 + 256 + 512
-    assert lib.moe_prefill_workspace_bytes(2, 8, 2, 64, 32, 2, 1) == 256 * 5 + 1024
+    # order, position, offsets, the gate and up scales in rows of 16, bfloat16 intermediate, bfloat16 rows, each
+    # rounded up to 256 bytes
+    assert need == 256 + 256 + 256 + 2 * 8 * 32 * 16 + 256 + 512
+    # float32 out: MXFP8 intermediate and its scales; the tokens' scales beside the matrices'
+    assert lib.moe_prefill_workspace_bytes(2, 8, 2, 64, 32, 2, 1) == 256 * 3 + (2 * 8 * 32 * 16 + 256) + 256 + 256 + 1024
+    assert lib.moe_prefill_workspace_bytes(2, 8, 2, 512, 640, 0, 0) == 256 * 3 + 4 * 640 * 2 + 4 * 512 * 2
     assert lib.moe_prefill_workspace_bytes(0, 8, 2, 64, 32, 0, 0) == 0
     assert lib.moe_prefill_workspace_bytes(2, 8, 2, 64, 33, 0, 0) == 0

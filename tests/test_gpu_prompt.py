@@ -210,7 +210,8 @@ COUNTS = {"few": [0, 1, 2, 0, 17, 5], "mid": [33, 0, 64, 65, 1, 130], "one": [0,
 @pytest.mark.parametrize("counts", list(COUNTS))
 @pytest.mark.parametrize("wformat", ["mxfp8", "mxfp4"])
 @pytest.mark.parametrize("act", ["bf16", "mxfp8"])
-@pytest.mark.parametrize("K,N", [(32, 32), (96, 64), (128, 160), (256, 256), (288, 96), (768, 512), (1024, 288)])
+@pytest.mark.parametrize("K,N", [(32, 32), (96, 64), (128, 160), (256, 256), (288, 96), (640, 128), (768, 512),
+                                 (1024, 288), (1120, 64)])
 def test_matmul_exact(counts, wformat, act, K, N):
     counts = COUNTS[counts]
     E, R = len(counts), sum(counts)
@@ -343,23 +344,30 @@ def test_product_bad_order_makes_nan_rows():
         assert (s[bad] == 255).all() and (s[keep] != 255).all()
 
 
-def test_product_scales_at_odd_addresses():
-    """Scale tensors are bytes: no alignment is asked of them."""
+@pytest.mark.parametrize("K", [256, 480, 512, 640, 896])
+def test_product_scales_at_dword_addresses(K):
+    """Scale tensors are bytes at any multiple of four."""
     g = gen(8)
     counts = [20, 140]
-    K, N, R = 512, 96, 160
+    N, R = 96, 160
     a, a_s = whole_mx(g, (R, K), "mxfp8")
     w_q, w_s = whole_mx(g, (2, N, K), "mxfp8")
     off = torch.tensor([0] + list(np.cumsum(counts)), dtype=torch.int32, device="cuda")
     ref = md.moe_grouped_matmul(a, off, w_q, w_s, a_s=a_s, out_dtype=torch.float32)
     assert torch.equal(ref, products64(decode(a, a_s), off, decode(w_q, w_s))[0].float())
-    for shift in (1, 2, 4, 7, 8):
-        def moved(t):
-            room = torch.empty(t.numel() + shift, dtype=torch.uint8, device="cuda")
-            room[shift:] = t.reshape(-1)
-            return room[shift:].view(t.shape)
-        out = md.moe_grouped_matmul(a, off, w_q, moved(w_s), a_s=moved(a_s), out_dtype=torch.float32)
+
+    def moved(t, shift):
+        room = torch.empty(t.numel() + shift, dtype=torch.uint8, device="cuda")
+        room[shift:] = t.reshape(-1)
+        return room[shift:].view(t.shape)
+
+    for shift in (4, 8, 12):
+        out = md.moe_grouped_matmul(a, off, w_q, moved(w_s, shift), a_s=moved(a_s, shift), out_dtype=torch.float32)
         assert torch.equal(out, ref), shift
+    for bad in ({"w_s": moved(w_s, 2), "a_s": a_s}, {"w_s": w_s, "a_s": moved(a_s, 1)}):
+        with pytest.raises(md.MoedError) as e:
+            md.moe_grouped_matmul(a, off, w_q, **bad)
+        assert e.value.status == md.MOED_ERR_ALIGN
 
 
 # ---------------------------------------------------------------------------- combine
