@@ -1,5 +1,7 @@
 // Products grouped by expert where experts have many rows (prompts): tiles of
 // rows x weight rows through LDS, matrix instructions on what it holds.
+#include <type_traits>
+
 #include "product_common.h"
 
 namespace moed {
@@ -30,6 +32,11 @@ __device__ __forceinline__ void load_to_lds16(const uint8_t* from, uint32_t base
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(base) : "memory");
 }
 
+__device__ __forceinline__ void load_to_lds4(const void* from, uint32_t base)
+{
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(from), "s"(base) : "memory");
+}
+
 template <int ROWS, bool FP4, int OUT, int RT, int NT, int WR, int WN>
 struct Shape {
     static constexpr bool kMX = ROWS == kRowsMX;
@@ -56,7 +63,9 @@ struct Shape {
     static constexpr bool inside(int out_frags) { return kWaves * 16 * scratch_row(out_frags) <= kRowBytes; }
     static constexpr int scratch_at(int out_frags) { return inside(out_frags) ? kRowBytes : kEnd; }
     static constexpr int bad_at(int out_frags) { return kEnd + (inside(out_frags) ? 0 : kWaves * 16 * scratch_row(out_frags)); }
-    static constexpr int lds(int out_frags) { return bad_at(out_frags) + 2 * kBM; }
+    static constexpr int slots_at(int out_frags) { return bad_at(out_frags) + 2 * kBM; }
+    static constexpr int kSlots = (kBM + kWave - 1) / kWave * kWave;
+    static constexpr int lds(int out_frags) { return slots_at(out_frags) + 4 * kSlots; }
     static_assert(kBM * kRU % kWave == 0 && kBN * kWU % kWave == 0, "whole loads per wavefront");
     static_assert((kThreads / kRU) % 8 == 0 && (kThreads / kWU) % 8 == 0, "a thread's loads share their place in the row");
     // loads of a step's weights by the wavefront that has the fewest
@@ -87,6 +96,20 @@ __device__ __forceinline__ int unit_at(int col, int c)
 
 __device__ __forceinline__ u32x4 lds16(const uint8_t* p) { return *reinterpret_cast<const u32x4*>(p); }
 
+// f(N) with the smallest of RT, RT/2, RT/4 .. (as a constant) that is at least
+// `live`: a tile's last rows take no more matrix instructions than they need.
+template <int RT, typename F>
+__device__ __forceinline__ void row_parts(int live, F&& f)
+{
+    if constexpr (RT >= 4) {
+        if (live <= RT / 2) {
+            row_parts<RT / 2>(live, f);
+            return;
+        }
+    }
+    f(std::integral_constant<int, RT>{});
+}
+
 // One tile: rows m0 .. of expert e, outputs n0 .. .
 struct Tile {
     int e, m0, n0, rows, row0;
@@ -114,26 +137,26 @@ moe_product_tiled_kernel(ProductArgs p, int nblk, int group_blocks)
     const int g = lane / 16, col = lane % 16;
     const int wr = w / WN, wn = w % WN;
     const int tiles = build_tiles<S::kThreads>(first, begin, p.offsets, p.E, p.R, S::kBM, wsum);
-    const long long items = (long long)tiles * nblk;
+    const int items = tiles * nblk;                           // below 2^31: checked by the host
     const size_t w_row = FP4 ? (size_t)p.K / 2 : (size_t)p.K, s_row = (size_t)p.s_row;
     const size_t a_row = ROWS == kRowsBF16 ? 2 * (size_t)p.K : (size_t)p.K;
     const uint32_t lds0 = (uint32_t)(size_t)(__attribute__((address_space(3))) uint8_t*)lds;
 
     // items of one expert are neighbours; within it blocks of weight rows in
     // groups, so that a group's weights and the expert's rows meet in one L2
-    auto find = [&](long long item) {
+    auto find = [&](int item) {
         Tile t;
         t.live = false;
         t.e = t.m0 = t.n0 = t.rows = t.row0 = 0;
-        if (item >= items)
+        if (item < 0 || item >= items)                        // negative: past 2^31
             return t;
-        const int e = tile_expert(first, p.E, (int)(item / nblk));
+        const int e = tile_expert(first, p.E, item / nblk);
         if (e >= p.E)
             return t;
         const int mt = first[e + 1] - first[e];
-        const long long local = item - (long long)first[e] * nblk;
-        const int grp = (int)(local / ((long long)group_blocks * mt));
-        const int rest = (int)(local - (long long)grp * group_blocks * mt);
+        const int local = item - first[e] * nblk;
+        const int grp = local / (group_blocks * mt);
+        const int rest = local - grp * group_blocks * mt;
         const int in_grp = nblk - grp * group_blocks < group_blocks ? nblk - grp * group_blocks : group_blocks;
         t.e = __builtin_amdgcn_readfirstlane(e);
         t.n0 = __builtin_amdgcn_readfirstlane((grp * group_blocks + rest % in_grp) * kNeurons);
@@ -148,57 +171,58 @@ moe_product_tiled_kernel(ProductArgs p, int nblk, int group_blocks)
     auto tile_row = [&](const Tile& t, int r) {                           // rows behind the last repeat it
         return t.row0 + (t.m0 + r < t.rows ? t.m0 + r : t.rows - 1);
     };
-    // slots of a tile: of this thread's row loads, and of its row's scales
-    auto sources = [&](const Tile& t, int (&src)[S::kRowLoads + 1]) {
+    // slots of a tile's rows, fetched to LDS while the tile before it is computed
+    const int* const slots = reinterpret_cast<const int*>(lds + S::slots_at(kOutFrags));
+    auto fetch_slots = [&](const Tile& t) {
+        if (p.order)
 #pragma unroll
-        for (int i = 0; i < S::kRowLoads; ++i)
-            src[i] = slot_of(p, tile_row(t, i * (S::kThreads / S::kRU) + tid / S::kRU));
-        src[S::kRowLoads] = 0;
-        if constexpr (ROWS != kRowsBF16) {
-            const int rr = (S::kScaleLoads - 1) * S::kThreads + tid;      // BN is a multiple of the threads, or below them
-            static_assert(S::kScaleLoads <= 2 && (S::kScaleLoads == 1 || S::kBN % S::kThreads == 0), "one row per thread");
-            if (rr >= S::kBN && rr < S::kScaleRows)
-                src[S::kRowLoads] = slot_of(p, tile_row(t, rr - S::kBN));
-        }
+            for (int i = 0; i < (S::kSlots + S::kThreads - 1) / S::kThreads; ++i)
+                if (i * S::kThreads + w * kWave < S::kSlots)
+                    load_to_lds4(p.order + tile_row(t, i * S::kThreads + tid),
+                                 lds0 + S::slots_at(kOutFrags) + (uint32_t)(i * S::kThreads + w * kWave) * 4u);
+    };
+    // row of `a` that row r of the tile reads, -1 for none
+    auto source = [&](const Tile& t, int r) {
+        return p.order ? source_row(p, slots[r]) : tile_row(t, r);
     };
 
     // Sources: uniform bases and 32-bit offsets (a wavefront's load of weights
     // lies within one fragment, so its matrix is uniform too); addresses for the
     // scales.
     const uint8_t *rbase = nullptr, *wbase = nullptr, *ubase = nullptr;
-    uint32_t roff[S::kRowLoads], woff[S::kWLoads];
+    uint32_t roff[S::kRowLoads], woff[S::kWLoads];            // woff: uniform, in rows
     const uint8_t* ssrc[S::kScaleLoads];
+    const uint32_t wlane = (uint32_t)(lane / S::kWU) * (uint32_t)w_row + 16u * wc;
     auto is_up = [&](int place) { return GLU && place / 16 % NT >= NT / 2; };       // place: weight row of the tile
-    auto weight_row = [&](const Tile& t, int place) {                               // row of its expert's matrix
+    // Row of its expert's matrix; N is a multiple of 32, so the 16 rows of a fragment lie before or behind its end
+    // together, and those behind repeat fragment 0 (they are not stored).
+    auto weight_row = [&](const Tile& t, int place) {
         const int f = place / 16 % NT;
         const int n = t.n0 + (place / (16 * NT) * kOutFrags + (GLU && f >= NT / 2 ? f - NT / 2 : f)) * 16 + place % 16;
-        return (uint32_t)(n < p.N ? n : p.N - 1);
+        return (uint32_t)(n < p.N ? n : place % 16);
     };
-    auto point = [&](const Tile& t, const int (&src)[S::kRowLoads + 1], int parity) {
+    auto point = [&](const Tile& t, int parity) {
         rbase = static_cast<const uint8_t*>(p.a) + (p.order ? 0 : (size_t)(t.row0 + t.m0) * a_row);
         const size_t m = (size_t)t.e * (size_t)p.N;
         wbase = p.w_q + m * w_row;
         if constexpr (GLU)
             ubase = p.u_q + m * w_row;
-        auto row_of = [&](int slot) {                         // rows behind rbase
-            return p.order ? source_row(p, slot) : slot - (t.row0 + t.m0);
-        };
 #pragma unroll
         for (int i = 0; i < S::kRowLoads; ++i) {
-            const int from = row_of(src[i]);
-            roff[i] = (uint32_t)(from < 0 ? 0 : from) * (uint32_t)a_row + 16u * rc;
             const int r = i * (S::kThreads / S::kRU) + tid / S::kRU;
+            const int from = source(t, r < S::kBM ? r : S::kBM - 1);
+            roff[i] = (uint32_t)(from < 0 ? 0 : p.order ? from : from - (t.row0 + t.m0)) * (uint32_t)a_row + 16u * rc;
             if (tid % S::kRU == 0 && r < S::kBM)
                 bad[parity * S::kBM + r] = from < 0;
         }
 #pragma unroll
-        for (int i = 0; i < S::kWLoads; ++i)
-            woff[i] = weight_row(t, i * (S::kThreads / S::kWU) + tid / S::kWU) * (uint32_t)w_row + 16u * wc;
+        for (int i = 0; i < S::kWLoads; ++i)                  // first of this wavefront's rows in load i
+            woff[i] = weight_row(t, i * (S::kThreads / S::kWU) + w * (kWave / S::kWU));
 #pragma unroll
         for (int i = 0; i < S::kScaleLoads; ++i) {
             const int place = i * S::kThreads + tid;
             if (ROWS != kRowsBF16 && place >= S::kBN) {
-                const int from = p.order ? source_row(p, src[S::kRowLoads]) : src[S::kRowLoads];
+                const int from = source(t, place - S::kBN < S::kBM ? place - S::kBN : S::kBM - 1);
                 ssrc[i] = p.a_s + (size_t)(from < 0 ? 0 : from) * s_row;
             } else {
                 const int at = place < S::kBN ? place : 0;
@@ -232,11 +256,11 @@ moe_product_tiled_kernel(ProductArgs p, int nblk, int group_blocks)
             if (S::kBN * S::kWU % S::kThreads != 0 && i * S::kThreads + w * kWave >= S::kBN * S::kWU)
                 continue;                                     // whole wavefronts
             const uint8_t* from = (is_up(i * (S::kThreads / S::kWU) + w * (kWave / S::kWU)) ? ubase : wbase) +
-                                  (size_t)st * (S::kWU * 16);
+                                  (size_t)woff[i] * w_row + (size_t)st * (S::kWU * 16);
             if (st < full)
-                load_to_lds16(from, woff[i], to + i * S::kThreads * 16);
+                load_to_lds16(from, wlane, to + i * S::kThreads * 16);
             else
-                load_to_lds16(in ? from + woff[i] : zeros, to + i * S::kThreads * 16);
+                load_to_lds16(in ? from + wlane : zeros, to + i * S::kThreads * 16);
         }
     };
     // Block scales are fetched 16 bytes (four steps) of a row at a time: a load
@@ -268,7 +292,8 @@ moe_product_tiled_kernel(ProductArgs p, int nblk, int group_blocks)
     constexpr int kWFrag = 16 * S::kWU * 16, kRFrag = 16 * S::kRU * 16;      // bytes of a fragment
     f32x4 acc[RT][NT];
     // One step's products . `release` is called once the step's weights and scales are in registers.
-    auto compute = [&](int st, auto release) {
+    auto compute = [&](int st, auto n, auto release) {
+        constexpr int N = decltype(n)::value;
         const uint8_t* wb = lds + S::kWAt + (st & 1) * S::kWBytes + w0;
         const uint8_t* rb = lds + (st & 1) * S::kRowBytes + r0;
         const int chunk = st / 4;
@@ -298,23 +323,23 @@ moe_product_tiled_kernel(ProductArgs p, int nblk, int group_blocks)
             for (int r = 0; r < RT; ++r)
                 asc[r] = rsb[r * 256];
 #pragma unroll
-            for (int r = 0; r < kAhead && r < RT; ++r)
+            for (int r = 0; r < kAhead && r < N; ++r)
                 read_a(r);
             release();
             __builtin_amdgcn_sched_barrier(0);
             // fragments of rows are read kAhead before their use, so that the reads of one pass under
             // the matrix instructions of the others
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                if (r + kAhead < RT)
-                    read_a(r + kAhead);
-                __builtin_amdgcn_sched_barrier(0);
+                    for (int r = 0; r < N; ++r) {
+                        if (r + kAhead < N)
+                            read_a(r + kAhead);
+                        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int f = 0; f < NT; ++f)
-                    acc[r][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        wv[f], av[r % (kAhead + 1)], acc[r][f], FP4 ? 4 : 0, 0, 0, wsc[f], 0, asc[r]);
-                __builtin_amdgcn_sched_barrier(0);
-            }
+                        for (int f = 0; f < NT; ++f)
+                            acc[r][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                                wv[f], av[r % (kAhead + 1)], acc[r][f], FP4 ? 4 : 0, 0, 0, wsc[f], 0, asc[r]);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
         } else {
             // lane group g multiplies the block 32g .. 32g+31 of the step, 8 values per instruction
             u32x4 wq[NT][FP4 ? 1 : 2];
@@ -336,78 +361,84 @@ moe_product_tiled_kernel(ProductArgs p, int nblk, int group_blocks)
             }
             release();
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                bf16x8 wv[NT];
+                    for (int q = 0; q < 4; ++q) {
+                        bf16x8 wv[NT];
 #pragma unroll
-                for (int f = 0; f < NT; ++f) {
-                    if constexpr (FP4) {
-                        wv[f] = decode8_scaled_fp4(wq[f][0][q], wsc[f]);
-                    } else {
-                        const u32x4 c = wq[f][q / 2];
-                        wv[f] = decode8_scaled((q & 1) ? u32x2{c.z, c.w} : u32x2{c.x, c.y}, wsc[f]);
+                        for (int f = 0; f < NT; ++f) {
+                            if constexpr (FP4) {
+                                wv[f] = decode8_scaled_fp4(wq[f][0][q], wsc[f]);
+                            } else {
+                                const u32x4 c = wq[f][q / 2];
+                                wv[f] = decode8_scaled((q & 1) ? u32x2{c.z, c.w} : u32x2{c.x, c.y}, wsc[f]);
+                            }
+                        }
+#pragma unroll
+                        for (int r = 0; r < N; ++r) {
+                            bf16x8 av;
+                            if constexpr (ROWS == kRowsMXExact) {
+                                const u32x4 c = lds16(rb + unit_at<8>(col, 2 * g + q / 2) + r * kRFrag);
+                                av = decode8_scaled((q & 1) ? u32x2{c.z, c.w} : u32x2{c.x, c.y}, asc[r]);
+                            } else {
+                                av = __builtin_bit_cast(bf16x8, lds16(rb + unit_at<16>(col, 4 * g + q) + r * kRFrag));
+                            }
+#pragma unroll
+                            for (int f = 0; f < NT; ++f)
+                                acc[r][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[f], av, acc[r][f], 0, 0, 0);
+                        }
                     }
-                }
-#pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    bf16x8 av;
-                    if constexpr (ROWS == kRowsMXExact) {
-                        const u32x4 c = lds16(rb + unit_at<8>(col, 2 * g + q / 2) + r * kRFrag);
-                        av = decode8_scaled((q & 1) ? u32x2{c.z, c.w} : u32x2{c.x, c.y}, asc[r]);
-                    } else {
-                        av = __builtin_bit_cast(bf16x8, lds16(rb + unit_at<16>(col, 4 * g + q) + r * kRFrag));
-                    }
-#pragma unroll
-                    for (int f = 0; f < NT; ++f)
-                        acc[r][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[f], av, acc[r][f], 0, 0, 0);
-                }
-            }
         }
     };
 
-    long long item = xcd_contiguous(blockIdx.x, gridDim.x);
+    int item = xcd_contiguous(blockIdx.x, gridDim.x);
     Tile t = find(item);
     int parity = 0;
+    if (t.live)
+        fetch_slots(t);
+    wait_loads<0>();
+    __syncthreads();
     if (t.live) {
-        int src[S::kRowLoads + 1];
-        sources(t, src);
-        point(t, src, 0);
+        point(t, 0);
         stage_first();
     }
-    while (item < items) {
-        Tile next = find(item + gridDim.x);
-        int nsrc[S::kRowLoads + 1];
+    while (item >= 0 && item < items) {
+        Tile next = find(item + (int)gridDim.x);
+        __syncthreads();                                      // everybody has this tile's slots
         if (next.live)
-            sources(next, nsrc);                              // used after this tile's steps
+            fetch_slots(next);
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
             for (int f = 0; f < NT; ++f)
                 acc[r][f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         if (t.live) {
-            for (int st = 0; st < steps; ++st) {
-                // A step's weights are asked for nearly two steps ahead (they come from far, and their buffer is
-                // free as soon as every wavefront has its fragments), its rows one step ahead. Step st is in LDS
-                // once this wavefront's loads of it, and then everybody's, are done.
-                if (st + 1 < steps)
-                    wait_loads<S::kWeightLoads>();
-                else
-                    wait_loads<0>();
-                __syncthreads();
-                if (st + 1 < steps)
-                    stage_rows(st + 1);
-                compute(st, [&] {
-                    __syncthreads();                          // everybody has the step's weights
-                    if ((st & 3) == 2 && st + 2 < steps)
-                        stage_scales(st / 4 + 1);
-                    if (st + 2 < steps)
-                        stage_weights(st + 2);
-                });
-            }
+            // row fragments of this wavefront that hold rows
+            row_parts<RT>((t.rows - t.m0 - wr * RT * 16 + 15) / 16, [&](auto n) {
+                for (int st = 0; st < steps; ++st) {
+                    // A step's weights are asked for nearly two steps ahead (they come from far, and their buffer is
+                    // free as soon as every wavefront has its fragments), its rows one step ahead. Step st is in LDS
+                    // once this wavefront's loads of it, and then everybody's, are done.
+                    if (st + 1 < steps)
+                        wait_loads<S::kWeightLoads>();
+                    else
+                        wait_loads<0>();
+                    __syncthreads();
+                    if (st + 1 < steps)
+                        stage_rows(st + 1);
+                    compute(st, n, [&] {
+                        __syncthreads();                          // everybody has the step's weights
+                        if ((st & 3) == 2 && st + 2 < steps)
+                            stage_scales(st / 4 + 1);
+                        if (st + 2 < steps)
+                            stage_weights(st + 2);
+                    });
+                }
+            });
         }
         // the next tile's first steps are on their way while this one is stored
+        wait_loads<0>();                                      // its slots, where this tile had no steps to wait in
         __syncthreads();
         if (next.live) {
-            point(next, nsrc, parity ^ 1);
+            point(next, parity ^ 1);
             stage_first();
         }
         if (t.live) {
@@ -415,6 +446,8 @@ moe_product_tiled_kernel(ProductArgs p, int nblk, int group_blocks)
             const int nw = t.n0 + wn * kOutFrags * 16;        // this wavefront's first output
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
+                if (t.m0 + (wr * RT + r) * 16 >= t.rows)
+                    break;
                 const bool none = bad[parity * S::kBM + (wr * RT + r) * 16 + col];
                 f32x4 o[kOutFrags];
 #pragma unroll
@@ -429,7 +462,7 @@ moe_product_tiled_kernel(ProductArgs p, int nblk, int group_blocks)
                 store_tile_rows<OUT, kOutFrags>(p, mine, kScratchRow, t.row0, t.m0 + (wr * RT + r) * 16, t.rows, nw, o);
             }
         }
-        item += gridDim.x;
+        item += (int)gridDim.x;
         t = next;
         parity ^= 1;
     }
