@@ -384,7 +384,8 @@ int moe_group(const int32_t *topk_ids, int B, int k, int E, int32_t *order,
  *            where that is 0 (K >= 512, a multiple of 128)
  * Rows from offsets[E] on stay as they were. out may not overlap a. Limits
  * (MOED_ERR_SHAPE): K and N positive multiples of 32, below 2^20, K*N below
- * 2^32; E <= 2048; R and n_a below 2^28; with an order, `a` below 4 GiB;
+ * 2^32; E <= 2048; R and n_a below 2^28; (R/16 + E)*N/32 below 2^31; with an
+ * order, `a` below 4 GiB;
  * k >= 1. a, out and the code pointers are 16-byte aligned, scales 4-byte
  * (MOED_ERR_ALIGN). R = 0 launches nothing.
  */

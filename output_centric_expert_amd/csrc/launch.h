@@ -140,7 +140,7 @@ struct CombineArgs {
     bool out_bf16;
 };
 hipError_t launch_combine(const CombineArgs& p, bool y_bf16, hipStream_t s);
-// Products grouped by expert over ragged rows (product_*.hip). The rows of
+// Products grouped by expert over ragged rows (product.hip and the files it calls). The rows of
 // expert e are offsets[e] .. offsets[e+1]-1; u_q set: SiLU(w row) * (u row).
 constexpr int kOutBF16 = 0, kOutF32 = 1, kOutMX8 = 2;
 struct ProductArgs {
@@ -163,7 +163,10 @@ struct ProductArgs {
 // 0: not needed).
 size_t product_scales_bytes(int E, int K, int N, int n_a, bool mx_rows, bool two);
 hipError_t launch_product(ProductArgs p, void* scales, hipStream_t s);
-hipError_t launch_product_tiled(const ProductArgs& p, int shape, hipStream_t s);
+// avg: rows an expert on average.
+hipError_t launch_product_bf16(const ProductArgs& p, int avg, hipStream_t s);
+hipError_t launch_product_mx(const ProductArgs& p, int avg, hipStream_t s);
+hipError_t launch_product_exact(const ProductArgs& p, int avg, hipStream_t s);
 // Opt-in input check (check.hip). Pointers not used by a step may be null:
 // the gate/up step passes no down matrix and the down step no gate/up ones.
 struct CheckArgs {

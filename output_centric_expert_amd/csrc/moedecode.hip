@@ -263,12 +263,20 @@ bool group_ok(int B, int k, int E)
            (long long)B * k < kMaxRows;
 }
 
+// The kernels number their tiles (of 16 rows and 32 outputs or more) with 31 bits.
+bool too_many_tiles(long long R, int E, int N)
+{
+    return (R / 16 + (R < E ? R : E)) * ((N + 31) / 32) >= (1LL << 31);
+}
+
 int check_product(int a_rows, int wfmt, int n_a, int k, bool ordered, int R, int E, int K, int N)
 {
     if (R < 0 || R >= kMaxRows || n_a < 0 || n_a >= kMaxRows || E < 1 || E > moed::kGroupMaxE || k < 1 ||
         (!ordered && n_a < R) || (R > 0 && n_a == 0))
         return MOED_ERR_SHAPE;
     if (K < 32 || N < 32 || K % 32 != 0 || N % 32 != 0 || K >= kMaxRowLength || N >= kMaxRowLength)
+        return MOED_ERR_SHAPE;
+    if (too_many_tiles(R, E, N))
         return MOED_ERR_SHAPE;
     // the kernels address one expert's matrix, and gathered rows, with 32-bit offsets
     if ((long long)K * N >= (1LL << 32) || (ordered && (long long)n_a * K * (a_rows == MOED_ROWS_BF16 ? 2 : 1) >= (1LL << 32)))
@@ -332,7 +340,7 @@ int prefill_layout(int B, int E, int k, int H, int I, int x_rows, int out_dtype,
     if ((x_rows != MOED_ROWS_BF16 && x_rows != MOED_ROWS_MXFP8) || !dtype_ok(out_dtype))
         return MOED_ERR_DTYPE;
     const bool mx = x_rows == MOED_ROWS_MXFP8;
-    if ((long long)H * I >= (1LL << 32) || (long long)B * H * (mx ? 1 : 2) >= (1LL << 32))
+    if (too_many_tiles((long long)B * k, E, H > I ? H : I) || (long long)H * I >= (1LL << 32) || (long long)B * H * (mx ? 1 : 2) >= (1LL << 32))
         return MOED_ERR_SHAPE;
     const size_t R = (size_t)B * (size_t)k;
     size_t at = 0;

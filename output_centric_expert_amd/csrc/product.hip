@@ -1,5 +1,5 @@
 // Products grouped by expert: the layout of the block scales and the choice of
-// the tile.
+// the kernel.
 #include "product_common.h"
 
 namespace moed {
@@ -77,8 +77,9 @@ hipError_t launch_product(ProductArgs p, void* scales, hipStream_t s)
     }
     const int experts = p.R < p.E ? p.R : p.E;
     const long long avg = ((long long)p.R + experts - 1) / experts;
-    const bool exact = p.a_s && p.out_kind == kOutF32;
-    return launch_product_tiled(p, avg >= 256 ? (p.a_s && !exact ? 0 : 2) : avg >= 96 ? 2 : avg >= 32 ? 4 : 7, s);
+    if (!p.a_s)
+        return launch_product_bf16(p, (int)avg, s);
+    return p.out_kind == kOutF32 ? launch_product_exact(p, (int)avg, s) : launch_product_mx(p, (int)avg, s);
 }
 
 }  // namespace moed

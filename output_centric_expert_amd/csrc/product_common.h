@@ -1,6 +1,5 @@
-// Shared parts of the products grouped by expert over ragged rows
-// (product_few.hip, product_tiled.hip): the list of row tiles, the operands of
-// one step of the matrix instructions, and the store of a tile.
+// Shared parts of the products grouped by expert over ragged rows: the list of
+// row tiles, the sources of rows, and the store of a tile.
 //
 // The matrix instructions take the weights as the A operand and the rows as the
 // B operand, so a lane receives four consecutive outputs of one row.
@@ -20,8 +19,6 @@
 namespace moed {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-
-constexpr int kProductMaxE = 2048;
 
 // first[e] = row tiles of the experts before e and begin[e] = first row of e
 // (E + 1 ints of LDS each), built by every workgroup. Offsets are clamped into

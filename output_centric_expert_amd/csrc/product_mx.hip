@@ -1,0 +1,78 @@
+// Products of MXFP8 rows with bfloat16 or MXFP8 outputs: codes and block scales enter the scaled matrix instructions
+// as they are stored.
+//
+// These instructions align the products of a few neighbouring k to the largest and drop what lies about 2^-20 of it
+// below: the sums are float32, their error measured 1.4e-5 of the result's norm whatever K and however the additions
+// are grouped. That is 1/280 of a bfloat16 rounding and 1/2000 of an E4M3 one; float32 outputs take product_exact.hip.
+#include "product_tiled.h"
+
+namespace moed {
+
+namespace {
+
+// The 256 x 256 tile leaves room in LDS for the tile list of that many experts.
+constexpr int kLargeTileMaxE = 1536;
+
+// The tile by the average of rows an expert (all the host knows). gate_up, K = 2048, N = 768, 8 of 128 experts, us of
+// the choices next to each other (8 wavefronts where not said; MXFP8 / MXFP4 weights):
+//   rows an expert              1         4         16        32        64         128        256
+//   16 x 128, 4 wavefronts    36 / 24   75 / 54   85 / 67  110 / 76  157 / 115  264 / 198  485 / 363
+//   16 x 256, 4 wavefronts    42 / 23   74 / 46   89 / 66  123 / 78  197 / 113  353 / 180  663 / 321
+//   64 x 256                  42 / 23   74 / 53   77 / 55   80 / 59  100 /  77  137 /  96  228 / 157
+//   128 x 128, 4 wavefronts   43 / 29   75 / 53   80 / 55   82 / 58   95 /  66  128 /  99  184 / 156
+//   128 x 256                 43 / 29   75 / 62   78 / 63   80 / 70   88 /  85  130 / 126  192 / 170
+//   256 x 256                 47 / 36   78 / 59   81 / 60   84 / 64   96 /  78  104 /  85  189 / 165
+// MXFP8 outputs need whole blocks of 32 in a wavefront (four fragments):
+//   16 x 128, 2 wavefronts    37 / 25   77 / 56   84 / 69  108 / 75  160 / 109  271 / 183  498 / 325
+//   32 x 256, 4 wavefronts    43 / 24   76 / 46   78 / 48   96 / 71  133 /  84  218 / 130  392 / 209
+//   64 x 256                  44 / 26   77 / 55   78 / 58   80 / 60  102 /  79  146 /  94  241 / 154
+//   128 x 128, 4 wavefronts   44 / 32   79 / 55   84 / 57   87 / 61  100 /  66  131 / 103  183 / 156
+//   128 x 256                 45 / 34   77 / 69   81 / 70   83 / 78   89 /  83  143 / 136  195 / 173
+//   256 x 256                 47 / 36   81 / 59   82 / 62   85 / 65   97 /  80  106 /  90  196 / 172
+template <bool FP4, bool GLU, int OUT>
+hipError_t by_rows(const ProductArgs& p, int avg, hipStream_t s)
+{
+    if (avg >= 96 && p.E <= kLargeTileMaxE)
+        return launch_shape<kRowsMX, FP4, GLU, OUT, 8, 4, 2, 4>(p, s);
+    if constexpr (OUT == kOutMX8) {
+        if (avg < 2)
+            return launch_shape<kRowsMX, FP4, GLU, OUT, 1, 4, 1, 2>(p, s);
+        if (avg < 24)
+            return launch_shape<kRowsMX, FP4, GLU, OUT, 2, 4, 1, 4>(p, s);
+        if (avg < 48)
+            return launch_shape<kRowsMX, FP4, GLU, OUT, 2, 4, 2, 4>(p, s);
+        if constexpr (FP4)
+            return launch_shape<kRowsMX, FP4, GLU, OUT, 4, 4, 2, 2>(p, s);
+        else
+            return launch_shape<kRowsMX, FP4, GLU, OUT, 4, 4, 2, 4>(p, s);
+    } else {
+        if constexpr (FP4)
+            if (avg < 8 && p.R >= 32)
+                return launch_shape<kRowsMX, FP4, GLU, OUT, 1, 4, 1, 4>(p, s);
+        if (avg < 2)
+            return launch_shape<kRowsMX, FP4, GLU, OUT, 1, 2, 1, 4>(p, s);
+        if (avg < 24)
+            return launch_shape<kRowsMX, FP4, GLU, OUT, 4, 2, 1, 8>(p, s);
+        if constexpr (FP4)
+            return launch_shape<kRowsMX, FP4, GLU, OUT, 8, 2, 1, 4>(p, s);
+        else
+            return launch_shape<kRowsMX, FP4, GLU, OUT, 8, 2, 1, 8>(p, s);
+    }
+}
+
+template <bool FP4>
+hipError_t by_out(const ProductArgs& p, int avg, hipStream_t s)
+{
+    if (!p.u_q)
+        return by_rows<FP4, false, kOutBF16>(p, avg, s);
+    return p.out_kind == kOutBF16 ? by_rows<FP4, true, kOutBF16>(p, avg, s) : by_rows<FP4, true, kOutMX8>(p, avg, s);
+}
+
+}  // namespace
+
+hipError_t launch_product_mx(const ProductArgs& p, int avg, hipStream_t s)
+{
+    return p.fp4 ? by_out<true>(p, avg, s) : by_out<false>(p, avg, s);
+}
+
+}  // namespace moed

@@ -1,19 +1,31 @@
-// Products grouped by expert where experts have many rows (prompts): tiles of
-// rows x weight rows through LDS, matrix instructions on what it holds.
+// The kernel of the products grouped by expert: tiles of rows x weight rows through LDS, matrix instructions on what
+// it holds. Included by one source file per kind of rows.
+//
+// A workgroup walks tiles (expert, rows, block of outputs) with a stride of the grid. A step is 128 values of K: its
+// weight rows, rows and block scales go from memory straight to LDS, two buffers of each; while a tile is stored, the
+// next one's first step is on its way. The mathematics is in product_common.h; what bounds a call:
+//  - up to about 50 rows an expert, the weights' bytes: 512 tokens of 8 of 128 experts, K = 2048, N = 768, gate and up
+//    in MXFP8 take 80 us with MXFP8 rows (5.3 TB/s of codes and scales), 83 us with bfloat16 rows;
+//  - beyond, the matrix instructions. With MXFP8 rows 8192 tokens take 298 us (1.38 PFLOP/s; the same loop without
+//    loads 224 us: the clock falls to 1.7 GHz under these instructions), of which the tiles' beginnings and ends are a
+//    quarter. With bfloat16 rows the decode of the weights (16 conversions for 4 * RT matrix instructions) comes on top.
+// What did not pay: fragments of the weights read straight from memory (a load of 16 rows x 64 bytes runs at a quarter
+// of the rate of one of 8 rows x 128 bytes); two groups of wavefronts taking turns between LDS and the matrix unit, and
+// loads spread among the matrix instructions (both wait longer for the loads than they save).
+#pragma once
+
 #include <type_traits>
 
 #include "product_common.h"
 
 namespace moed {
 
-namespace {
-
 // How rows enter the matrix instructions.
 constexpr int kRowsBF16 = 0;      // bfloat16 rows, weights decoded to bfloat16
 constexpr int kRowsMX = 1;        // MXFP8 rows and MX weights as stored, scaled matrix instructions
 constexpr int kRowsMXExact = 2;   // MXFP8 rows and weights both decoded to bfloat16
 
-__device__ const u32x4 kZeros = {0, 0, 0, 0};     // source of the values behind the end of a row
+static __device__ const u32x4 kZeros = {0, 0, 0, 0};   // source of the values behind the end of a row
 
 // 16 bytes per lane from global memory straight to LDS: lane i of the wavefront
 // writes base + 16 i (base uniform). No register receives the data; the caller
@@ -115,8 +127,6 @@ struct Tile {
     int e, m0, n0, rows, row0;
     bool live;
 };
-
-}  // namespace
 
 template <int ROWS, bool FP4, bool GLU, int OUT, int RT, int NT, int WR, int WN>
 __global__ void __launch_bounds__(WR * WN * kWave)
@@ -468,8 +478,6 @@ moe_product_tiled_kernel(ProductArgs p, int nblk, int group_blocks)
     }
 }
 
-namespace {
-
 template <int ROWS, bool FP4, bool GLU, int OUT, int RT, int NT, int WR, int WN>
 hipError_t launch_shape(const ProductArgs& p, hipStream_t s)
 {
@@ -494,58 +502,6 @@ hipError_t launch_shape(const ProductArgs& p, hipStream_t s)
     hipLaunchKernelGGL((moe_product_tiled_kernel<ROWS, FP4, GLU, OUT, RT, NT, WR, WN>), dim3((unsigned)grid),
                        dim3(S::kThreads), lds, s, p, nblk, (int)group);
     return hipGetLastError();
-}
-
-template <int ROWS, bool FP4, bool GLU, int OUT>
-hipError_t tiled_shape(const ProductArgs& p, int shape, hipStream_t s)
-{
-    constexpr bool M = ROWS == kRowsMX, B = ROWS == kRowsBF16;
-    switch (shape) {
-    case 0: if constexpr (M) return launch_shape<ROWS, FP4, GLU, OUT, 8, 4, 2, 4>(p, s); break;   // 256 x 256
-    case 1: return launch_shape<ROWS, FP4, GLU, OUT, 4, 4, 2, 4>(p, s);       // 128 x 256
-    case 2: return launch_shape<ROWS, FP4, GLU, OUT, 4, 4, 2, 2>(p, s);       // 128 x 128
-    case 3: return launch_shape<ROWS, FP4, GLU, OUT, 4, 4, 1, 4>(p, s);       // 64 x 256
-    case 4: return launch_shape<ROWS, FP4, GLU, OUT, 2, 4, 2, 2>(p, s);       // 64 x 128
-    case 5: return launch_shape<ROWS, FP4, GLU, OUT, 4, 4, 1, 2>(p, s);       // 64 x 128, 2 waves
-    case 6: return launch_shape<ROWS, FP4, GLU, OUT, 2, 4, 1, 4>(p, s);       // 32 x 256
-    case 7: return launch_shape<ROWS, FP4, GLU, OUT, 1, 4, 1, 4>(p, s);       // 16 x 256
-    case 8: return launch_shape<ROWS, FP4, GLU, OUT, 1, 4, 1, 2>(p, s);       // 16 x 128
-    case 9: return launch_shape<ROWS, FP4, GLU, OUT, 2, 4, 1, 2>(p, s);       // 32 x 128
-    case 10: if constexpr (M||B) return launch_shape<ROWS, FP4, GLU, OUT, 8, 4, 1, 4>(p, s); break;       // 128 x 256, 4 waves
-    case 11: if constexpr (M||B) return launch_shape<ROWS, FP4, GLU, OUT, 8, 4, 1, 2>(p, s); break;       // 128 x 128, 2 waves
-    }
-    return hipErrorInvalidValue;
-}
-
-template <bool FP4>
-hipError_t tiled_rows(const ProductArgs& p, int shape, hipStream_t s)
-{
-    if (p.u_q) {
-        if (!p.a_s) {
-            if (p.out_kind == kOutBF16)
-                return tiled_shape<kRowsBF16, FP4, true, kOutBF16>(p, shape, s);
-            if (p.out_kind == kOutF32)
-                return tiled_shape<kRowsBF16, FP4, true, kOutF32>(p, shape, s);
-            return tiled_shape<kRowsBF16, FP4, true, kOutMX8>(p, shape, s);
-        }
-        if (p.out_kind == kOutBF16)
-            return tiled_shape<kRowsMX, FP4, true, kOutBF16>(p, shape, s);
-        if (p.out_kind == kOutF32)
-            return tiled_shape<kRowsMXExact, FP4, true, kOutF32>(p, shape, s);
-        return tiled_shape<kRowsMX, FP4, true, kOutMX8>(p, shape, s);
-    }
-    if (!p.a_s)
-        return p.out_kind == kOutBF16 ? tiled_shape<kRowsBF16, FP4, false, kOutBF16>(p, shape, s)
-                                      : tiled_shape<kRowsBF16, FP4, false, kOutF32>(p, shape, s);
-    return p.out_kind == kOutBF16 ? tiled_shape<kRowsMX, FP4, false, kOutBF16>(p, shape, s)
-                                  : tiled_shape<kRowsMXExact, FP4, false, kOutF32>(p, shape, s);
-}
-
-}  // namespace
-
-hipError_t launch_product_tiled(const ProductArgs& p, int shape, hipStream_t s)
-{
-    return p.fp4 ? tiled_rows<true>(p, shape, s) : tiled_rows<false>(p, shape, s);
 }
 
 }  // namespace moed

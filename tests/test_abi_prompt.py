@@ -62,7 +62,7 @@ def matmul(lib, a=A, a_s=None, rows=0, n_a=8, order=A, k=2, off=A, wq=A, ws=A, w
 def test_products_reject(lib, call):  # noqa: F811
     assert call(lib, R=0) == md.MOED_OK
     for kw in ({"R": -1}, {"R": 1 << 28}, {"n_a": -1}, {"n_a": 0}, {"k": 0}, {"E": 0}, {"E": 2049}, {"K": 48}, {"N": 40},
-               {"K": 0}, {"N": 1 << 20}, {"order": None}, {"K": 1 << 16, "N": 1 << 16}, {"n_a": 1 << 22}):
+               {"K": 0}, {"N": 1 << 20}, {"order": None}, {"K": 1 << 16, "N": 1 << 16}, {"n_a": 1 << 22}, {"R": (1 << 28) - 1, "N": 8192}):
         assert call(lib, **kw) == md.MOED_ERR_SHAPE, kw
     for kw in ({"rows": 1}, {"rows": 3}, {"wf": 2}, {"out_rows": 3}, {"out_rows": -1}):
         assert call(lib, **kw) == md.MOED_ERR_DTYPE, kw

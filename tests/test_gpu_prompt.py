@@ -204,7 +204,8 @@ def test_group_skewed_and_empty():
 
 # rows per expert: empty experts, single rows, whole and part tiles, one expert with everything
 COUNTS = {"few": [0, 1, 2, 0, 17, 5], "mid": [33, 0, 64, 65, 1, 130], "one": [0, 0, 300], "single": [1],
-          "large": [700, 0, 257, 256, 3, 128, 1025], "even": [64] * 40}
+          "large": [700, 0, 257, 256, 3, 128, 1025], "even": [64] * 40, "ones": [1] * 10 + [0] * 3, "threes": [3] * 40,
+          "some": [20, 33, 7, 18, 22], "forty": [40, 1, 79]}
 
 
 @pytest.mark.parametrize("counts", list(COUNTS))
@@ -370,6 +371,63 @@ def test_product_scales_at_dword_addresses(K):
         assert e.value.status == md.MOED_ERR_ALIGN
 
 
+@pytest.mark.parametrize("E", [1537, 2048])
+def test_product_many_experts(E):
+    """Average row counts of the largest tile, with more experts than its tile list has room for."""
+    K, N = 128, 32
+    g = gen(E)
+    counts = np.random.default_rng(E).integers(60, 160, E)
+    R = int(counts.sum())
+    a, a_s = whole_mx(g, (R, K), "mxfp8")
+    w_q, w_s = whole_mx(g, (E, N, K), "mxfp4")
+    off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+    wv, av = decode(w_q, w_s, "mxfp4"), decode(a, a_s)
+    out = md.moe_grouped_matmul(a, off, w_q, w_s, a_s=a_s, wformat="mxfp4")
+    e = expert_rows(off, R)
+    for some in torch.arange(R, device="cuda").split(20000):
+        ref = (wv[e[some]] @ av[some][..., None]).squeeze(-1)
+        assert torch.equal(out[some], ref.float().to(torch.bfloat16))
+
+
+def test_product_past_32_bits():
+    """More than 2^32 bytes of outputs, and of rows in place."""
+    K, N, R = 128, 32736, 70001
+    g = gen(77)
+    a, a_s = whole_mx(g, (R, K), "mxfp8")
+    w_q, w_s = whole_mx(g, (2, N, K), "mxfp8")
+    off = torch.tensor([0, 5, R], dtype=torch.int32, device="cuda")
+    out = md.moe_grouped_matmul(a, off, w_q, w_s, a_s=a_s)
+    assert out.numel() > 2 ** 31
+    wv = decode(w_q, w_s)
+    for r in (0, 4, 5, 33333, 65599, 65600, R - 1):
+        assert torch.equal(out[r], (wv[int(r >= 5)] @ decode(a[r:r + 1], a_s[r:r + 1])[0]).float().to(torch.bfloat16)), r
+    del out
+    rows = torch.empty((70000, 32768), dtype=torch.bfloat16, device="cuda")
+    rows[-300:] = torch.randint(-4, 5, (300, 32768), generator=g, device="cuda").to(torch.bfloat16)
+    rows[:-300] = 0
+    w_q, w_s = whole_mx(g, (1, 32, 32768), "mxfp4")
+    out = md.moe_grouped_matmul(rows, torch.tensor([0, 70000], dtype=torch.int32, device="cuda"), w_q, w_s,
+                                out_dtype=torch.float32, wformat="mxfp4")
+    ref = rows[-300:].double() @ decode(w_q, w_s, "mxfp4")[0].T
+    assert torch.equal(out[-300:], ref.float()) and (out[:-300] == 0).all()
+    with pytest.raises(md.MoedError):            # gathered rows of 4 GiB and more are refused
+        md.moe_grouped_matmul(rows, torch.tensor([0, 4], dtype=torch.int32, device="cuda"), w_q, w_s,
+                              order=torch.arange(4, dtype=torch.int32, device="cuda"), wformat="mxfp4")
+
+
+def test_product_offsets_that_make_no_sense():
+    """Decreasing, negative and too large offsets: wrong rows, but the call ends and other rows stay as they were."""
+    g = gen(12)
+    K, N, R = 128, 64, 500
+    a = torch.ones(R, K, dtype=torch.bfloat16, device="cuda")
+    w_q, w_s = whole_mx(g, (4, N, K), "mxfp8")
+    for off in ([0, 300, 100, 400, 450], [-5, 10, 20, 2 ** 31 - 1, 7], [500, 500, 500, 500, 500], [2 ** 31 - 1] * 5, [-1] * 5):
+        out = torch.full((R + 2, N), 9.0, dtype=torch.float32, device="cuda")
+        md.moe_grouped_matmul(a, torch.tensor(off, dtype=torch.int32, device="cuda"), w_q, w_s, out=out[:R])
+        torch.cuda.synchronize()
+        assert (out[R:] == 9.0).all()
+
+
 # ---------------------------------------------------------------------------- combine
 
 @pytest.mark.parametrize("B,k,H", [(1, 8, 2048), (3, 1, 7), (5, 64, 33), (300, 8, 4096), (17, 9, 2056), (2, 3, 8)])
@@ -383,6 +441,22 @@ def test_combine(B, k, H, dtype):
     out = md.moe_combine(y, pos, w, out_dtype=torch.float32)
     assert ((out.double() - terms.sum(1)).abs() <= (k + 1) * U * terms.abs().sum(1)).all()
     assert torch.equal(bits(md.moe_combine(y, pos, w)), bits(out.to(torch.bfloat16)))
+
+
+def test_norm_and_combine_past_32_bits():
+    B, H = 140000, 16384
+    x = torch.empty((B, H), dtype=torch.bfloat16, device="cuda")
+    x.fill_(1.0)
+    x[-1] = torch.randn(H, generator=gen(1), device="cuda").to(torch.bfloat16)
+    gain = torch.ones(H, device="cuda")
+    out, _, q, s = md.moe_norm(x, gain, quantize=True)
+    for b in (0, 131071, 131072, B - 1):
+        one, _, q1, s1 = md.moe_norm(x[b:b + 1].clone(), gain, quantize=True)
+        assert torch.equal(bits(out[b]), bits(one[0])) and torch.equal(q[b], q1[0]) and torch.equal(s[b], s1[0])
+    pos = torch.tensor([[0, B - 1], [131072, 131071]], dtype=torch.int32, device="cuda")
+    w = torch.tensor([[1.0, 2.0], [0.5, 0.25]], device="cuda")
+    got = md.moe_combine(x, pos, w, out_dtype=torch.float32)
+    assert torch.equal(got[0], x[0].float() + 2 * x[-1].float()) and (got[1] == 0.75).all()
 
 
 def test_combine_bad_positions():
