@@ -25,10 +25,10 @@ __device__ __forceinline__ void fetch(const void* y, size_t at, Piece<BF16, V>& 
     if constexpr (V == 1) {
         p.a.x = BF16 ? (uint32_t)static_cast<const uint16_t*>(y)[at] << 16 : static_cast<const uint32_t*>(y)[at];
     } else if constexpr (BF16) {
-        p.a = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(y) + at);
+        p.a = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(y) + at));
     } else {
-        p.a = *reinterpret_cast<const u32x4*>(static_cast<const float*>(y) + at);
-        p.b = *reinterpret_cast<const u32x4*>(static_cast<const float*>(y) + at + 4);
+        p.a = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(static_cast<const float*>(y) + at));
+        p.b = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(static_cast<const float*>(y) + at + 4));
     }
 }
 

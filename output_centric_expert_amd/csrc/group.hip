@@ -34,6 +34,18 @@ __device__ __forceinline__ unsigned long long same_id(int id, int bits, unsigned
     return m;
 }
 
+// Adds expert e's counts of blocks from .. to-1 (`earlier`: of those before blk).
+__device__ __forceinline__ void add_counts(const int32_t* counts, int e, int E, int from, int to, int blk, int& earlier,
+                                           int& all)
+{
+#pragma unroll 8
+    for (int q = from; q < to; ++q) {
+        const int c = counts[(size_t)q * E + e];
+        earlier += q < blk ? c : 0;
+        all += c;
+    }
+}
+
 // Sum of v over the threads before this one, and over all (block of 1024).
 __device__ __forceinline__ int block_exclusive(int v, int* wsum, int& total)
 {
@@ -93,6 +105,7 @@ moe_group_place_kernel(const int32_t* ids, int n, int E, int bits, int nblk, con
     extern __shared__ int start[];                // E: first place of this block's slots of each expert
     uint16_t* cnt = reinterpret_cast<uint16_t*>(start + E);    // [16][E]
     __shared__ int wsum[kGroupWavesN];
+    __shared__ int sums[2 * kGroupThreads];
     const int tid = threadIdx.x, lane = tid % kWave, w = tid / kWave;
     const int blk = blockIdx.x;
     const long long first = (long long)blk * (PER * kGroupThreads) + (long long)w * (PER * kWave) + lane;
@@ -123,6 +136,19 @@ moe_group_place_kernel(const int32_t* ids, int n, int E, int bits, int nblk, con
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
     __syncthreads();
+    // few experts: the blocks' counts are added by parts = 1024 / E threads an expert
+    const int parts = nblk > 1 && E < kGroupThreads ? kGroupThreads / E : 1;
+    if (parts > 1) {
+        const int q = tid / E, e = tid - q * E;
+        if (q < parts) {
+            int earlier = 0, all = 0;
+            const int per = (nblk + parts - 1) / parts;
+            add_counts(counts, e, E, q * per, q * per + per < nblk ? q * per + per : nblk, blk, earlier, all);
+            sums[(2 * q) * E + e] = earlier;
+            sums[(2 * q + 1) * E + e] = all;
+        }
+        __syncthreads();
+    }
     // per expert: earlier wavefronts of this block, earlier blocks, all blocks
     int done = 0;                                 // slots of the experts before this chunk of 1024 experts
     for (int e0 = 0; e0 < E; e0 += kGroupThreads) {
@@ -137,11 +163,12 @@ moe_group_place_kernel(const int32_t* ids, int n, int E, int bits, int nblk, con
             }
             if (nblk == 1) {
                 all = mine;
-            } else {
-                for (int q = 0; q < nblk; ++q) {
-                    const int c = counts[(size_t)q * E + e];
-                    earlier += q < blk ? c : 0;
-                    all += c;
+            } else if (parts == 1) {
+                add_counts(counts, e, E, 0, nblk, blk, earlier, all);
+            } else {                              // E <= 512: summed above by all threads
+                for (int q = 0; q < parts; ++q) {
+                    earlier += sums[(2 * q) * E + e];
+                    all += sums[(2 * q + 1) * E + e];
                 }
             }
         }

@@ -28,21 +28,21 @@ namespace {
 __device__ __forceinline__ float bf16_val(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
 
 // V consecutive values of a bf16 or float32 array as float32.
-template <bool BF16, int V>
+template <bool BF16, bool NT, int V>
 __device__ __forceinline__ void load_vals(const void* p, size_t at, float (&v)[V])
 {
     if constexpr (V == 1) {
         v[0] = BF16 ? bf16_val(static_cast<const uint16_t*>(p)[at]) : static_cast<const float*>(p)[at];
     } else if constexpr (BF16) {
-        const u32x4 u = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + at);
+        const u32x4 u = ld<NT>(reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + at));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v[2 * i] = bf16_lo(u[i]);
             v[2 * i + 1] = bf16_hi(u[i]);
         }
     } else {
-        const f32x4 a = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + at);
-        const f32x4 b = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + at + 4);
+        const f32x4 a = ld<NT>(reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + at));
+        const f32x4 b = ld<NT>(reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + at + 4));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v[i] = a[i];
@@ -89,10 +89,10 @@ moe_norm_kernel(NormArgs p)
     for (int i = 0; i < NV; ++i) {
         const int h = (t + i * TPR) * V;
         if (h < p.H) {
-            load_vals<XBF16>(p.x, row + h, s[i]);
+            load_vals<XBF16, true>(p.x, row + h, s[i]);
             if constexpr (RES != 0) {
                 float r[V];
-                load_vals<RES == 1>(p.residual, row + h, r);
+                load_vals<RES == 1, true>(p.residual, row + h, r);
 #pragma unroll
                 for (int v = 0; v < V; ++v)
                     s[i][v] += r[v];
@@ -130,9 +130,9 @@ moe_norm_kernel(NormArgs p)
                 store_vals<RES == 1>(p.residual_out, row + h, s[i]);
         float g[V];
         if (p.gain_bf16)
-            load_vals<true>(p.gain, (size_t)h, g);
+            load_vals<true, false>(p.gain, (size_t)h, g);
         else
-            load_vals<false>(p.gain, (size_t)h, g);
+            load_vals<false, false>(p.gain, (size_t)h, g);
         float y[V];
 #pragma unroll
         for (int v = 0; v < V; ++v)

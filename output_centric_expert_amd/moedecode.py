@@ -350,7 +350,8 @@ def _raw_stream(stream, dev):
 
 def _new(shape, dtype, x, stream):
     """A tensor made here for a call on `stream`: its memory is not handed out again before that work is done."""
-    t = torch.empty(shape, dtype=dtype, device=x.device)
+    # the cheapest of torch's ways: these calls wait for the host as long as for the GPU
+    t = torch.empty_like(x) if x.dtype is dtype and x.shape == shape and x.is_contiguous() else x.new_empty(shape, dtype=dtype)
     if stream is not None:
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=x.device)
@@ -408,9 +409,10 @@ def moe_group(topk_ids, E: int, order=None, position=None, offsets=None, workspa
     order = _new((B * k,), torch.int32, topk_ids, stream) if order is None else order
     position = _new((B, k), torch.int32, topk_ids, stream) if position is None else position
     offsets = _new((E + 1,), torch.int32, topk_ids, stream) if offsets is None else offsets
-    need = int(load().moe_group_workspace_bytes(B, k, E))
-    if workspace is None and need:
-        workspace = _new((need,), torch.uint8, topk_ids, stream)
+    if workspace is None:
+        need = int(load().moe_group_workspace_bytes(B, k, E))
+        if need:
+            workspace = _new((need,), torch.uint8, topk_ids, stream)
     st = load().moe_group(
         _arg(topk_ids, "topk_ids", _I32, (B, k), dev), B, k, E, _arg(order, "order", _I32, (B * k,), dev),
         _arg(position, "position", _I32, (B, k), dev), _arg(offsets, "offsets", _I32, (E + 1,), dev),
