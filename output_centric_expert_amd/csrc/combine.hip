@@ -101,7 +101,7 @@ moe_combine_kernel(CombineArgs p)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             u[i] = f32x2_to_bf16x2_rne(acc[2 * i], acc[2 * i + 1]);
-        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.out) + at) = u;
+        __builtin_nontemporal_store(u, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.out) + at));
     } else {
         *reinterpret_cast<f32x4*>(static_cast<float*>(p.out) + at) = f32x4{acc[0], acc[1], acc[2], acc[3]};
         *reinterpret_cast<f32x4*>(static_cast<float*>(p.out) + at + 4) = f32x4{acc[4], acc[5], acc[6], acc[7]};

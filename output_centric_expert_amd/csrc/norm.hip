@@ -64,10 +64,10 @@ __device__ __forceinline__ void store_vals(void* p, size_t at, const float (&v)[
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             u[i] = f32x2_to_bf16x2_rne(v[2 * i], v[2 * i + 1]);
-        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + at) = u;
+        __builtin_nontemporal_store(u, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + at));
     } else {
-        *reinterpret_cast<f32x4*>(static_cast<float*>(p) + at) = f32x4{v[0], v[1], v[2], v[3]};
-        *reinterpret_cast<f32x4*>(static_cast<float*>(p) + at + 4) = f32x4{v[4], v[5], v[6], v[7]};
+        __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4*>(static_cast<float*>(p) + at));
+        __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, reinterpret_cast<f32x4*>(static_cast<float*>(p) + at + 4));
     }
 }
 
@@ -156,7 +156,7 @@ moe_norm_kernel(NormArgs p)
                 const uint32_t c = mx8_scale_code(m);
                 codes.x = mx8_codes4(y[0], y[1], y[2], y[3], c);
                 codes.y = mx8_codes4(y[4], y[5], y[6], y[7], c);
-                *reinterpret_cast<u32x2*>(p.q + row + h) = codes;
+                __builtin_nontemporal_store(codes, reinterpret_cast<u32x2*>(p.q + row + h));
                 if ((t & 3) == 0)
                     p.q_s[(row + h) / 32] = (uint8_t)c;
             }
