@@ -21,22 +21,22 @@ hipError_t by_rows(const ProductArgs& p, int avg, hipStream_t s)
 {
     if constexpr (OUT == kOutMX8) {
         if (avg < 4)
-            return launch_shape<kRowsBF16, FP4, GLU, OUT, 1, 4, 1, 2>(p, s);
+            return launch_shape<kRowsBF16, FP4, GLU, OUT, 1, 4, 1, 2>(p, avg, s);
         if (FP4 || avg < 48)
-            return launch_shape<kRowsBF16, FP4, GLU, OUT, 4, 4, 1, 4>(p, s);
+            return launch_shape<kRowsBF16, FP4, GLU, OUT, 4, 4, 1, 4>(p, avg, s);
         if constexpr (!FP4)
-            return launch_shape<kRowsBF16, FP4, GLU, OUT, 4, 4, 2, 4>(p, s);
+            return launch_shape<kRowsBF16, FP4, GLU, OUT, 4, 4, 2, 4>(p, avg, s);
     } else {
         if (avg < 4)
-            return launch_shape<kRowsBF16, FP4, GLU, OUT, 1, 2, 1, 4>(p, s);
+            return launch_shape<kRowsBF16, FP4, GLU, OUT, 1, 2, 1, 4>(p, avg, s);
         if constexpr (FP4) {
             if (avg < 48)
-                return launch_shape<kRowsBF16, FP4, GLU, OUT, 4, 2, 1, 4>(p, s);
-            return launch_shape<kRowsBF16, FP4, GLU, OUT, 4, 2, 1, 8>(p, s);
+                return launch_shape<kRowsBF16, FP4, GLU, OUT, 4, 2, 1, 4>(p, avg, s);
+            return launch_shape<kRowsBF16, FP4, GLU, OUT, 4, 2, 1, 8>(p, avg, s);
         } else {
             if (avg < 32)
-                return launch_shape<kRowsBF16, FP4, GLU, OUT, 4, 2, 1, 8>(p, s);
-            return launch_shape<kRowsBF16, FP4, GLU, OUT, 8, 2, 1, 8>(p, s);
+                return launch_shape<kRowsBF16, FP4, GLU, OUT, 4, 2, 1, 8>(p, avg, s);
+            return launch_shape<kRowsBF16, FP4, GLU, OUT, 8, 2, 1, 8>(p, avg, s);
         }
     }
     return hipErrorInvalidValue;

@@ -20,18 +20,18 @@ hipError_t by_rows(const ProductArgs& p, int avg, hipStream_t s)
 {
     if constexpr (FP4) {
         if (avg < 4 && p.R < 32)
-            return launch_shape<kRowsMXExact, FP4, GLU, kOutF32, 1, 2, 1, 4>(p, s);
+            return launch_shape<kRowsMXExact, FP4, GLU, kOutF32, 1, 2, 1, 4>(p, avg, s);
         if (avg < 8)
-            return launch_shape<kRowsMXExact, FP4, GLU, kOutF32, 1, 4, 1, 4>(p, s);
+            return launch_shape<kRowsMXExact, FP4, GLU, kOutF32, 1, 4, 1, 4>(p, avg, s);
         if (avg < 24)
-            return launch_shape<kRowsMXExact, FP4, GLU, kOutF32, 2, 2, 1, 8>(p, s);
-        return launch_shape<kRowsMXExact, FP4, GLU, kOutF32, 4, 2, 1, 4>(p, s);
+            return launch_shape<kRowsMXExact, FP4, GLU, kOutF32, 2, 2, 1, 8>(p, avg, s);
+        return launch_shape<kRowsMXExact, FP4, GLU, kOutF32, 4, 2, 1, 4>(p, avg, s);
     } else {
         if (avg < 4)
-            return launch_shape<kRowsMXExact, FP4, GLU, kOutF32, 1, 2, 1, 4>(p, s);
+            return launch_shape<kRowsMXExact, FP4, GLU, kOutF32, 1, 2, 1, 4>(p, avg, s);
         if (avg < 48)
-            return launch_shape<kRowsMXExact, FP4, GLU, kOutF32, 4, 2, 1, 4>(p, s);
-        return launch_shape<kRowsMXExact, FP4, GLU, kOutF32, 8, 2, 1, 4>(p, s);
+            return launch_shape<kRowsMXExact, FP4, GLU, kOutF32, 4, 2, 1, 4>(p, avg, s);
+        return launch_shape<kRowsMXExact, FP4, GLU, kOutF32, 8, 2, 1, 4>(p, avg, s);
     }
 }
 

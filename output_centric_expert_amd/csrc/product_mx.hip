@@ -33,30 +33,30 @@ template <bool FP4, bool GLU, int OUT>
 hipError_t by_rows(const ProductArgs& p, int avg, hipStream_t s)
 {
     if (avg >= 96 && p.E <= kLargeTileMaxE)
-        return launch_shape<kRowsMX, FP4, GLU, OUT, 8, 4, 2, 4>(p, s);
+        return launch_shape<kRowsMX, FP4, GLU, OUT, 8, 4, 2, 4>(p, avg, s);
     if constexpr (OUT == kOutMX8) {
         if (avg < 2)
-            return launch_shape<kRowsMX, FP4, GLU, OUT, 1, 4, 1, 2>(p, s);
+            return launch_shape<kRowsMX, FP4, GLU, OUT, 1, 4, 1, 2>(p, avg, s);
         if (avg < 24)
-            return launch_shape<kRowsMX, FP4, GLU, OUT, 2, 4, 1, 4>(p, s);
+            return launch_shape<kRowsMX, FP4, GLU, OUT, 2, 4, 1, 4>(p, avg, s);
         if (avg < 48)
-            return launch_shape<kRowsMX, FP4, GLU, OUT, 2, 4, 2, 4>(p, s);
+            return launch_shape<kRowsMX, FP4, GLU, OUT, 2, 4, 2, 4>(p, avg, s);
         if constexpr (FP4)
-            return launch_shape<kRowsMX, FP4, GLU, OUT, 4, 4, 2, 2>(p, s);
+            return launch_shape<kRowsMX, FP4, GLU, OUT, 4, 4, 2, 2>(p, avg, s);
         else
-            return launch_shape<kRowsMX, FP4, GLU, OUT, 4, 4, 2, 4>(p, s);
+            return launch_shape<kRowsMX, FP4, GLU, OUT, 4, 4, 2, 4>(p, avg, s);
     } else {
         if constexpr (FP4)
             if (avg < 8 && p.R >= 32)
-                return launch_shape<kRowsMX, FP4, GLU, OUT, 1, 4, 1, 4>(p, s);
+                return launch_shape<kRowsMX, FP4, GLU, OUT, 1, 4, 1, 4>(p, avg, s);
         if (avg < 2)
-            return launch_shape<kRowsMX, FP4, GLU, OUT, 1, 2, 1, 4>(p, s);
+            return launch_shape<kRowsMX, FP4, GLU, OUT, 1, 2, 1, 4>(p, avg, s);
         if (avg < 24)
-            return launch_shape<kRowsMX, FP4, GLU, OUT, 4, 2, 1, 8>(p, s);
+            return launch_shape<kRowsMX, FP4, GLU, OUT, 4, 2, 1, 8>(p, avg, s);
         if constexpr (FP4)
-            return launch_shape<kRowsMX, FP4, GLU, OUT, 8, 2, 1, 4>(p, s);
+            return launch_shape<kRowsMX, FP4, GLU, OUT, 8, 2, 1, 4>(p, avg, s);
         else
-            return launch_shape<kRowsMX, FP4, GLU, OUT, 8, 2, 1, 8>(p, s);
+            return launch_shape<kRowsMX, FP4, GLU, OUT, 8, 2, 1, 8>(p, avg, s);
     }
 }
 
