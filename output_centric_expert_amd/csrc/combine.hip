@@ -2,11 +2,13 @@
 // float32 accumulator, one store. A position outside [0, R) makes the token's
 // outputs NaN (no read is made for it).
 //
-// Memory bound: k rows in, one row out. A thread owns V neighbouring outputs of
-// one token and asks for up to kAhead rows' values before it adds the first;
-// the positions and weights are uniform over the workgroup and load as scalars.
-#include "launch.h"
+// Memory bound: k rows in, one row out (8192 tokens, 8 rows of 2048 bfloat16
+// values each: 302 MB in 50 us, 6.0 TB/s; 60 us without streaming loads and
+// stores). A thread owns V neighbouring outputs of one token and asks for up to
+// kAhead rows' values before it adds the first; the positions and weights are
+// uniform over the workgroup and load as scalars.
 #include "mx_device.h"
+#include "prompt.h"
 
 namespace moed {
 

@@ -11,6 +11,7 @@
 namespace moed {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kGroupWaves = 4;                  // wavefronts per workgroup, 16 neurons each
 constexpr int kGroupNeurons = 16 * kGroupWaves;

@@ -14,12 +14,14 @@
 //
 // A row is read once and stays in registers between the two passes of the
 // formula (V values per load, NV loads per thread, TPR threads per row), so the
-// kernel moves each input and output byte once and is bound by memory, or by
-// the latency of one load and one reduction for a single token. With 8 values
-// per thread an MX block is four neighbouring lanes, whose largest value is
-// found with two DPP steps.
-#include "launch.h"
-#include "mx_device.h"
+// kernel moves each input and output byte once. It is bound by memory: 8192
+// tokens of 4096 values, residual and MXFP8 included, take 49.4 us (303 MB at
+// 6.1 TB/s; a 2 GiB copy reaches 6.35). Loads and stores are streaming (cached:
+// 58 us). A single token is bound by one load and one reduction (1.9 us in a
+// graph). With 8 values per thread an MX block is four neighbouring lanes,
+// whose largest value is found with two DPP steps.
+#include "mx_encode.h"
+#include "prompt.h"
 
 namespace moed {
 
@@ -188,6 +190,7 @@ hipError_t launch_shape(const NormArgs& p, bool x_bf16, int res, hipStream_t s)
 hipError_t launch_norm(const NormArgs& p, bool x_bf16, int res, hipStream_t s)
 {
     const int H = p.H;
+    // rows of a multiple of 8 values are whole 16-byte pieces; others go by single values
     if (H % 8 == 0) {
         if (H <= 2048 && p.B >= 2048)
             return launch_shape<8, 4, 64>(p, x_bf16, res, s);

@@ -15,6 +15,8 @@
 #pragma once
 
 #include "grouped_common.h"
+#include "mx_encode.h"
+#include "prompt.h"
 
 namespace moed {
 

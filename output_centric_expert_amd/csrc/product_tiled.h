@@ -486,7 +486,7 @@ hipError_t launch_shape(const ProductArgs& p, int avg, hipStream_t s)
     constexpr int kNeurons = 16 * kOutFrags * WN;
     const size_t lds = S::lds(kOutFrags) + ((size_t)p.E + 1) * 8;
     const void* f = reinterpret_cast<const void*>(&moe_product_tiled_kernel<ROWS, FP4, GLU, OUT, RT, NT, WR, WN>);
-    if (lds > 65536)
+    if (lds > 49152)
         if (hipError_t e = set_max_dynamic_lds(f, (int)lds))
             return e;
     const int nblk = (p.N + kNeurons - 1) / kNeurons;

@@ -171,7 +171,7 @@ def test_norm_special_values():
 # ---------------------------------------------------------------------------- group
 
 @pytest.mark.parametrize("B,k,E", [(1, 1, 1), (1, 8, 128), (64, 8, 256), (3, 5, 67), (128, 8, 9), (129, 8, 9), (1000, 8, 128),
-                                   (1024, 8, 2048), (1025, 8, 2048), (4097, 3, 31), (16384, 8, 128), (33000, 8, 64),
+                                   (1024, 8, 2048), (1025, 8, 2048), (500, 8, 1700), (4097, 3, 31), (16384, 8, 128), (33000, 8, 64),
                                    (262144, 1, 3), (262145, 1, 1000), (7, 64, 64)])
 @pytest.mark.parametrize("bad", [False, True])
 def test_group(B, k, E, bad):
@@ -569,6 +569,13 @@ def test_prefill_check_mode(monkeypatch):
     with pytest.raises(md.MoedError) as e:
         md.moe_prefill(x, ids, w, *mats)
     assert e.value.status == md.MOED_ERR_SCALE
+    # MXFP8 rows take any scale in the gate and up matrices; in the down matrix only where float32 is not asked for
+    hq, hs = quantize(x.float())
+    md.moe_prefill(hq, ids, w, *mats, x_s=hs, out_dtype=torch.float32)
+    mats[5][int(ids[0, 0]), 3, 0] = 250
+    md.moe_prefill(hq, ids, w, *mats, x_s=hs)
+    with pytest.raises(md.MoedError):
+        md.moe_prefill(hq, ids, w, *mats, x_s=hs, out_dtype=torch.float32)
 
 
 def run_block(x, r, gain, logits, mats, k, ws=None, stream=None):
@@ -617,6 +624,20 @@ def test_block_on_two_streams_at_once():
         for (_, a), b in zip(got, want):
             for u, v in zip(a, b):
                 assert torch.equal(bits(u), bits(v))
+
+
+def test_raw_stream_handle():
+    """A stream given as its handle, with everything made inside the calls."""
+    x, logits, mats = layer_inputs(30, 16, 4, 288, 96, "mxfp8", 91)
+    x = x.to(torch.bfloat16)
+    gain, r = torch.ones(288, device="cuda"), torch.zeros(30, 288, dtype=torch.bfloat16, device="cuda")
+    want = run_block(x, r, gain, logits, mats, 4)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = run_block(x, r, gain, logits, mats, 4, stream=side.cuda_stream)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(bits(a), bits(b))
 
 
 def test_results_repeat():
