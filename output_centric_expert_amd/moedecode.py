@@ -363,6 +363,15 @@ def _new(shape, dtype, x, stream):
     return t
 
 
+def _result(t, name, dtypes, shape, dev, dtype, x, stream):
+    """(result, address): the caller's tensor, checked, or a new one of `dtype`."""
+    if t is None:
+        t = _new(shape, dtype, x, stream)
+        if t.dtype in dtypes and t.get_device() == dev:
+            return t, t.data_ptr()
+    return t, _arg(t, name, dtypes, shape, dev)
+
+
 _U8, _I32, _F32, _BF = (torch.uint8,), (torch.int32,), (torch.float32,), (torch.bfloat16,)
 _F = (torch.bfloat16, torch.float32)
 
@@ -380,22 +389,22 @@ def moe_norm(x, gain, residual=None, eps: float = 1e-6, out_dtype=torch.bfloat16
     B, H = x.shape
     if quantize and H % 32:
         raise ValueError("quantize needs H to be a multiple of 32")
-    if out is None and out_dtype is not None:
-        out = _new((B, H), out_dtype, x, stream)
-    if residual is not None and residual_out is None:
-        residual_out = _new((B, H), residual.dtype, x, stream)
+    xp, gp, rp, r_dtype = _arg(x, "x", _F, (B, H), dev), _arg(gain, "gain", _F, (H,), dev), None, MOED_BF16
+    op = rop = qp = sp = None
+    if residual is not None:
+        rp, r_dtype = _arg(residual, "residual", _F, (B, H), dev), _DT[residual.dtype]
+        residual_out, rop = _result(residual_out, "residual_out", (residual.dtype,), (B, H), dev, residual.dtype, x, stream)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    if out is not None or out_dtype is not None:
+        out, op = _result(out, "out", _F, (B, H), dev, out_dtype, x, stream)
     if quantize:
-        out_q = _new((B, H), torch.uint8, x, stream) if out_q is None else out_q
-        out_s = _new((B, H // 32), torch.uint8, x, stream) if out_s is None else out_s
+        out_q, qp = _result(out_q, "out_q", _U8, (B, H), dev, torch.uint8, x, stream)
+        out_s, sp = _result(out_s, "out_s", _U8, (B, H // 32), dev, torch.uint8, x, stream)
     elif out_q is not None or out_s is not None:
         raise ValueError("out_q and out_s need quantize=True")
-    st = load().moe_norm(
-        _arg(x, "x", _F, (B, H), dev), _DT[x.dtype], _opt(residual, "residual", _F, (B, H), dev),
-        _DT[residual.dtype] if residual is not None else MOED_BF16, _arg(gain, "gain", _F, (H,), dev), _DT[gain.dtype],
-        float(eps), _opt(residual_out, "residual_out", (residual.dtype,) if residual is not None else _F, (B, H), dev),
-        _opt(out, "out", _F, (B, H), dev), _DT[out.dtype] if out is not None else MOED_BF16,
-        _opt(out_q, "out_q", _U8, (B, H), dev), _opt(out_s, "out_s", _U8, (B, H // 32), dev),
-        B, H, _raw_stream(stream, dev))
+    st = load().moe_norm(xp, _DT[x.dtype], rp, r_dtype, gp, _DT[gain.dtype], eps, rop, op,
+                         _DT[out.dtype] if out is not None else MOED_BF16, qp, sp, B, H, _raw_stream(stream, dev))
     _check(st, "moe_norm")
     return out, residual_out, out_q, out_s
 
@@ -406,18 +415,16 @@ def moe_group(topk_ids, E: int, order=None, position=None, offsets=None, workspa
     if topk_ids.dim() != 2:
         raise ValueError("topk_ids: expected shape [B, k]")
     B, k = topk_ids.shape
-    order = _new((B * k,), torch.int32, topk_ids, stream) if order is None else order
-    position = _new((B, k), torch.int32, topk_ids, stream) if position is None else position
-    offsets = _new((E + 1,), torch.int32, topk_ids, stream) if offsets is None else offsets
+    ip = _arg(topk_ids, "topk_ids", _I32, None, dev)
+    order, op = _result(order, "order", _I32, (B * k,), dev, torch.int32, topk_ids, stream)
+    position, pp = _result(position, "position", _I32, (B, k), dev, torch.int32, topk_ids, stream)
+    offsets, fp = _result(offsets, "offsets", _I32, (E + 1,), dev, torch.int32, topk_ids, stream)
     if workspace is None:
         need = int(load().moe_group_workspace_bytes(B, k, E))
         if need:
             workspace = _new((need,), torch.uint8, topk_ids, stream)
-    st = load().moe_group(
-        _arg(topk_ids, "topk_ids", _I32, (B, k), dev), B, k, E, _arg(order, "order", _I32, (B * k,), dev),
-        _arg(position, "position", _I32, (B, k), dev), _arg(offsets, "offsets", _I32, (E + 1,), dev),
-        _opt(workspace, "workspace", _U8, None, dev), workspace.numel() if workspace is not None else 0,
-        _raw_stream(stream, dev))
+    wp = _opt(workspace, "workspace", _U8, None, dev)
+    st = load().moe_group(ip, B, k, E, op, pp, fp, wp, 0 if wp is None else workspace.numel(), _raw_stream(stream, dev))
     _check(st, "moe_group")
     return order, position, offsets
 
@@ -508,12 +515,10 @@ def moe_combine(y, position, topk_w, out=None, out_dtype=torch.bfloat16, stream=
         raise ValueError("expected y [R, H] and position [B, k]")
     R, H = y.shape
     B, k = position.shape
-    if out is None:
-        out = _new((B, H), out_dtype, y, stream)
-    st = load().moe_combine(
-        _arg(y, "y", _F, (R, H), dev), _DT[y.dtype], R, _arg(position, "position", _I32, (B, k), dev),
-        _arg(topk_w, "topk_w", _F32, (B, k), dev), _arg(out, "out", _F, (B, H), dev), _DT[out.dtype], B, k, H,
-        _raw_stream(stream, dev))
+    yp, pp, wp = (_arg(y, "y", _F, None, dev), _arg(position, "position", _I32, None, dev),
+                  _arg(topk_w, "topk_w", _F32, (B, k), dev))
+    out, op = _result(out, "out", _F, (B, H), dev, out_dtype, y, stream)
+    st = load().moe_combine(yp, _DT[y.dtype], R, pp, wp, op, _DT[out.dtype], B, k, H, _raw_stream(stream, dev))
     _check(st, "moe_combine")
     return out
 
