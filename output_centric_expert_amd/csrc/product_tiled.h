@@ -6,9 +6,10 @@
 // next one's first step is on its way. The mathematics is in product_common.h; what bounds a call:
 //  - up to about 50 rows an expert, the weights' bytes: 512 tokens of 8 of 128 experts, K = 2048, N = 768, gate and up
 //    in MXFP8 take 80 us with MXFP8 rows (5.3 TB/s of codes and scales), 83 us with bfloat16 rows;
-//  - beyond, the matrix instructions. With MXFP8 rows 8192 tokens take 298 us (1.38 PFLOP/s; the same loop without
-//    loads 224 us: the clock falls to 1.7 GHz under these instructions), of which the tiles' beginnings and ends are a
-//    quarter. With bfloat16 rows the decode of the weights (16 conversions for 4 * RT matrix instructions) comes on top.
+//  - beyond, the matrix instructions. With MXFP8 rows 8192 tokens take 280-288 us (1.43-1.47 PFLOP/s; the same loop
+//    without loads 224 us: the clock falls to 1.7 GHz under these instructions), of which the tiles' beginnings and ends
+//    are a sixth. With bfloat16 rows the decode of the weights (16 conversions for 4 * RT matrix instructions) comes on
+//    top.
 // What did not pay: fragments of the weights read straight from memory (a load of 16 rows x 64 bytes runs at a quarter
 // of the rate of one of 8 rows x 128 bytes); two groups of wavefronts taking turns between LDS and the matrix unit, and
 // loads spread among the matrix instructions (both wait longer for the loads than they save).
@@ -173,7 +174,7 @@ moe_product_tiled_kernel(ProductArgs p, int nblk, int group_blocks, int contiguo
         t.m0 = __builtin_amdgcn_readfirstlane((rest / in_grp) * S::kBM);
         t.row0 = __builtin_amdgcn_readfirstlane(begin[t.e]);
         t.rows = __builtin_amdgcn_readfirstlane(begin[t.e + 1]) - t.row0;
-        t.live = t.m0 >= 0 && t.m0 < t.rows && t.n0 >= 0 && t.n0 < p.N;   // false only for offsets that decrease
+        t.live = t.m0 < t.rows && t.n0 < p.N;
         return t;
     };
     const int rc = (tid % S::kRU) ^ swizzle<S::kRU>(tid / S::kRU);        // this thread's unit within a row and step
@@ -301,7 +302,8 @@ moe_product_tiled_kernel(ProductArgs p, int nblk, int group_blocks, int contiguo
     const int w0 = wn * NT * 16 * S::kWU * 16, r0 = wr * RT * 16 * S::kRU * 16;
     constexpr int kWFrag = 16 * S::kWU * 16, kRFrag = 16 * S::kRU * 16;      // bytes of a fragment
     f32x4 acc[RT][NT];
-    // One step's products . `release` is called once the step's weights and scales are in registers.
+    // One step's products for the first n fragments of rows. `release` is called once the step's weights and scales are
+    // in registers.
     auto compute = [&](int st, auto n, auto release) {
         constexpr int N = decltype(n)::value;
         const uint8_t* wb = lds + S::kWAt + (st & 1) * S::kWBytes + w0;
@@ -340,16 +342,16 @@ moe_product_tiled_kernel(ProductArgs p, int nblk, int group_blocks, int contiguo
             // fragments of rows are read kAhead before their use, so that the reads of one pass under
             // the matrix instructions of the others
 #pragma unroll
-                    for (int r = 0; r < N; ++r) {
-                        if (r + kAhead < N)
-                            read_a(r + kAhead);
-                        __builtin_amdgcn_sched_barrier(0);
+            for (int r = 0; r < N; ++r) {
+                if (r + kAhead < N)
+                    read_a(r + kAhead);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                        for (int f = 0; f < NT; ++f)
-                            acc[r][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                                wv[f], av[r % (kAhead + 1)], acc[r][f], FP4 ? 4 : 0, 0, 0, wsc[f], 0, asc[r]);
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
+                for (int f = 0; f < NT; ++f)
+                    acc[r][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        wv[f], av[r % (kAhead + 1)], acc[r][f], FP4 ? 4 : 0, 0, 0, wsc[f], 0, asc[r]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         } else {
             // lane group g multiplies the block 32g .. 32g+31 of the step, 8 values per instruction
             u32x4 wq[NT][FP4 ? 1 : 2];
@@ -371,31 +373,31 @@ moe_product_tiled_kernel(ProductArgs p, int nblk, int group_blocks, int contiguo
             }
             release();
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        bf16x8 wv[NT];
+            for (int q = 0; q < 4; ++q) {
+                bf16x8 wv[NT];
 #pragma unroll
-                        for (int f = 0; f < NT; ++f) {
-                            if constexpr (FP4) {
-                                wv[f] = decode8_scaled_fp4(wq[f][0][q], wsc[f]);
-                            } else {
-                                const u32x4 c = wq[f][q / 2];
-                                wv[f] = decode8_scaled((q & 1) ? u32x2{c.z, c.w} : u32x2{c.x, c.y}, wsc[f]);
-                            }
-                        }
-#pragma unroll
-                        for (int r = 0; r < N; ++r) {
-                            bf16x8 av;
-                            if constexpr (ROWS == kRowsMXExact) {
-                                const u32x4 c = lds16(rb + unit_at<8>(col, 2 * g + q / 2) + r * kRFrag);
-                                av = decode8_scaled((q & 1) ? u32x2{c.z, c.w} : u32x2{c.x, c.y}, asc[r]);
-                            } else {
-                                av = __builtin_bit_cast(bf16x8, lds16(rb + unit_at<16>(col, 4 * g + q) + r * kRFrag));
-                            }
-#pragma unroll
-                            for (int f = 0; f < NT; ++f)
-                                acc[r][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[f], av, acc[r][f], 0, 0, 0);
-                        }
+                for (int f = 0; f < NT; ++f) {
+                    if constexpr (FP4) {
+                        wv[f] = decode8_scaled_fp4(wq[f][0][q], wsc[f]);
+                    } else {
+                        const u32x4 c = wq[f][q / 2];
+                        wv[f] = decode8_scaled((q & 1) ? u32x2{c.z, c.w} : u32x2{c.x, c.y}, wsc[f]);
                     }
+                }
+#pragma unroll
+                for (int r = 0; r < N; ++r) {
+                    bf16x8 av;
+                    if constexpr (ROWS == kRowsMXExact) {
+                        const u32x4 c = lds16(rb + unit_at<8>(col, 2 * g + q / 2) + r * kRFrag);
+                        av = decode8_scaled((q & 1) ? u32x2{c.z, c.w} : u32x2{c.x, c.y}, asc[r]);
+                    } else {
+                        av = __builtin_bit_cast(bf16x8, lds16(rb + unit_at<16>(col, 4 * g + q) + r * kRFrag));
+                    }
+#pragma unroll
+                    for (int f = 0; f < NT; ++f)
+                        acc[r][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[f], av, acc[r][f], 0, 0, 0);
+                }
+            }
         }
     };
 

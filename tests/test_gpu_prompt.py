@@ -410,6 +410,12 @@ def test_product_past_32_bits():
                                 out_dtype=torch.float32, wformat="mxfp4")
     ref = rows[-300:].double() @ decode(w_q, w_s, "mxfp4")[0].T
     assert torch.equal(out[-300:], ref.float()) and (out[:-300] == 0).all()
+    # gathered rows between 2 and 4 GiB: 32-bit offsets without a sign
+    last = rows[-65535:]
+    order = torch.tensor([65244, 2, 65534], dtype=torch.int32, device="cuda")
+    out = md.moe_grouped_matmul(last, torch.tensor([0, 3], dtype=torch.int32, device="cuda"), w_q, w_s, order=order,
+                                out_dtype=torch.float32, wformat="mxfp4")
+    assert torch.equal(out, (last[order.long()].double() @ decode(w_q, w_s, "mxfp4")[0].T).float())
     with pytest.raises(md.MoedError):            # gathered rows of 4 GiB and more are refused
         md.moe_grouped_matmul(rows, torch.tensor([0, 4], dtype=torch.int32, device="cuda"), w_q, w_s,
                               order=torch.arange(4, dtype=torch.int32, device="cuda"), wformat="mxfp4")
