@@ -343,6 +343,8 @@ typedef enum {
  * block of 32 is max(floor(log2 amax) - 8 + 127, 0), 0 for a block of zeros;
  * codes are y / 2^(scale-127) saturated to +-448 and rounded to nearest even;
  * a block that holds an infinity or a NaN gets scale 255 and NaN codes.
+ * The squares are summed in float32: a row whose sum passes its range (values
+ * from about 1e19) has y = 0.
  * Limits (MOED_ERR_SHAPE): 1 <= H <= 32768, eps >= 0; H a multiple of 32 with
  * out_q. Pointers of x, residual, gain, residual_out, out and out_q are
  * 16-byte aligned (MOED_ERR_ALIGN). B = 0 launches nothing.
@@ -391,9 +393,8 @@ int moe_group(const int32_t *topk_ids, int B, int k, int E, int32_t *order,
  * Rows from offsets[E] on stay as they were. out may not overlap a. Limits
  * (MOED_ERR_SHAPE): K and N positive multiples of 32, below 2^20, K*N below
  * 2^32; E <= 2048; R and n_a below 2^28; (R/16 + E)*N/32 below 2^31; with an
- * order, `a` below 4 GiB;
- * k >= 1. a, out and the code pointers are 16-byte aligned, scales 4-byte
- * (MOED_ERR_ALIGN). R = 0 launches nothing.
+ * order, `a` below 4 GiB; k >= 1. a, out and the code pointers are 16-byte
+ * aligned, scales 4-byte (MOED_ERR_ALIGN). R = 0 launches nothing.
  */
 int moe_grouped_gate_up(const void *a, const uint8_t *a_s, int a_rows, int n_a,
                         const int32_t *order, int k, const int32_t *offsets,

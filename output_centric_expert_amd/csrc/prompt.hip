@@ -98,7 +98,8 @@ int prefill_layout(int B, int E, int k, int H, int I, int x_rows, int out_dtype,
     if ((x_rows != MOED_ROWS_BF16 && x_rows != MOED_ROWS_MXFP8) || !dtype_ok(out_dtype))
         return MOED_ERR_DTYPE;
     const bool mx = x_rows == MOED_ROWS_MXFP8;
-    if (too_many_tiles((long long)B * k, E, H > I ? H : I) || (long long)H * I >= (1LL << 32) || (long long)B * H * (mx ? 1 : 2) >= (1LL << 32))
+    if (too_many_tiles((long long)B * k, E, H > I ? H : I) || (long long)H * I >= (1LL << 32) ||
+        (long long)B * H * (mx ? 1 : 2) >= (1LL << 32))
         return MOED_ERR_SHAPE;
     const size_t R = (size_t)B * (size_t)k;
     size_t at = 0;

@@ -27,8 +27,8 @@ EXPORTS = ("moed_workspace_bytes", "moe_decode", "moe_decode_gate_up", "moe_deco
            "moed_selftest_decode", "moed_bench_read", "moed_bench_copy", "moed_status_string",
            "moed_last_hip_error", "moed_tuning_init", "moe_decode_tuned", "moe_decode_gate_up_tuned",
            "moe_decode_down_tuned", "moe_decode_noalloc", "moed_bench_read_cfg", "moe_norm",
-           "moe_group_workspace_bytes", "moe_group", "moe_grouped_workspace_bytes", "moe_grouped_gate_up", "moe_grouped_matmul", "moe_combine",
-           "moe_prefill_workspace_bytes", "moe_prefill")
+           "moe_group_workspace_bytes", "moe_group", "moe_grouped_workspace_bytes", "moe_grouped_gate_up",
+           "moe_grouped_matmul", "moe_combine", "moe_prefill_workspace_bytes", "moe_prefill")
 
 
 class MoedTuning(ctypes.Structure):
@@ -475,6 +475,8 @@ def moe_grouped_gate_up(a, offsets, wg_q, wg_s, wu_q, wu_s, order=None, k: int =
     if quantize:
         out = _new((R, N), torch.uint8, a, stream) if out is None else out
         out_s = _new((R, N // 32), torch.uint8, a, stream) if out_s is None else out_s
+    elif out_s is not None:
+        raise ValueError("out_s needs quantize=True")
     elif out is None:
         out = _new((R, N), out_dtype, a, stream)
     wp, wb, workspace = _product_workspace(workspace, E, K, N, a.shape[0], a_rows, 2, a, dev, stream)

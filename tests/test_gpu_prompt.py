@@ -701,8 +701,20 @@ def test_binding_refusals():
         md.moe_grouped_matmul(x, off, w_q, w_s, wformat="mxfp4")
     with pytest.raises(TypeError):
         md.moe_grouped_matmul(x, off, w_q, w_s, a_s=w_s[0])       # bfloat16 rows with scales
+    with pytest.raises(ValueError):                               # scales of an output that is not MXFP8
+        md.moe_grouped_gate_up(x, off, w_q, w_s, w_q, w_s, out_s=torch.zeros(4, 1, dtype=torch.uint8, device="cuda"))
     with pytest.raises(md.MoedError):
         md.moe_grouped_matmul(x, off, w_q, w_s, order=torch.zeros(4, dtype=torch.int32, device="cuda"), k=0)
     with pytest.raises(md.MoedError):
         room = torch.zeros(2 * 32 * 64 + 4, dtype=torch.uint8, device="cuda")
         md.moe_grouped_matmul(x, off, room[4:].view(2, 32, 64), w_s)
+
+
+def test_norm_past_the_range():
+    """Squares whose float32 sum is infinite: zeros, and the sum with the residual as it is."""
+    x = torch.full((2, 64), 2.0 ** 70, device="cuda")
+    x[1] = 1.0
+    out, res, q, s = md.moe_norm(x, torch.ones(64, device="cuda"), residual=x, eps=0.0, out_dtype=torch.float32, quantize=True)
+    assert (out[0] == 0).all() and (q[0] == 0).all() and (s[0] == 0).all()
+    # row 1: one unit in the last place of the reciprocal root, one rounding of the product
+    assert torch.equal(res, 2 * x) and ((out[1] - 1).abs() <= 2.0 ** -22).all()
