@@ -313,10 +313,13 @@ int moed_bench_read_cfg(const void *src, size_t bytes, void *sink, size_t sink_b
  *    exact.
  *  - MXFP8 rows, BFLOAT16 or MXFP8 outputs: codes and block scales (any) enter
  *    the scaled matrix instructions as stored. These drop, among the products
- *    of a few neighbouring k, what lies about 2^-20 below the largest: about
- *    1.4e-5 of the result in the 2-norm, 1/280 of a BFLOAT16 rounding.
+ *    of a few neighbouring k, what lies about 2^-20 below the largest: with
+ *    normal values 1.5e-5 of the result in the 2-norm (MXFP4 weights: 4e-6),
+ *    1/260 of a BFLOAT16 rounding. An output next to a border between two
+ *    rounded values can take the neighbour (0.2 % of the MXFP8 codes).
  *  - MXFP8 rows, FLOAT32 outputs: rows and weights are both decoded to
- *    BFLOAT16, so the range of scale codes applies to both.
+ *    BFLOAT16, so the range of scale codes applies to both; these are the
+ *    outputs to ask for where sums as good as float32's are needed.
  * Results are deterministic; how rows are tiled goes by the call's sizes, so a
  * row's low bits can differ between calls of different sizes.
  */

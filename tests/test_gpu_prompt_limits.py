@@ -1,0 +1,187 @@
+"""GPU tests of the prompt-side operators at the ends of their ranges: block scales of every size, NaN and the
+error of the scaled matrix instructions (MXFP8 rows with bfloat16 or MXFP8 outputs).
+
+What those instructions drop measured 1.4e-5 to 1.5e-5 of the result in the 2-norm with normal values. It is a sum of
+many small parts, so a single output is held to ten times that, of the 2-norm of its own terms, and a 2-norm over
+thousands of outputs to twice that. Rounding keeps order, so an output whose unrounded value lies within d of the
+exact y lies between the roundings of y - d and y + d."""
+import numpy as np
+import pytest
+import torch
+
+from output_centric_expert_amd import moedecode as md
+from test_gpu_prompt import COUNTS, U, decode, gen, gpu, products64, quantize, random_mx, whole_mx  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+DROPPED = 1.4e-5
+
+
+def ones(shape, fmt):
+    """Codes of 1.0."""
+    K = shape[-1] if fmt == "mxfp8" else shape[-1] // 2
+    return torch.full((*shape[:-1], K), 0x38 if fmt == "mxfp8" else 0x22, dtype=torch.uint8, device="cuda")
+
+
+def offsets_of(counts):
+    return torch.tensor([0] + list(np.cumsum(counts)), dtype=torch.int32, device="cuda")
+
+
+# ---------------------------------------------------------------------------- scaled matrix instructions
+
+SCALES = (0, 1, 2, 10, 54, 60, 64, 100, 126, 127, 128, 150, 190, 245, 253, 254, 255)
+
+
+@pytest.mark.parametrize("K", [96, 128, 512, 1152])
+@pytest.mark.parametrize("wformat", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("rows_each", [1, 40])
+def test_scaled_product_takes_every_scale(K, wformat, rows_each):
+    """Every pair of a row's and a weight's scale code: K * 2^(s + t - 254), NaN where either is 255."""
+    a_s = torch.tensor(SCALES, dtype=torch.uint8, device="cuda").repeat_interleave(rows_each)
+    R, N = a_s.numel(), 32
+    w_s = torch.full((N,), 127, dtype=torch.uint8, device="cuda")
+    w_s[:len(SCALES)] = torch.tensor(SCALES, dtype=torch.uint8, device="cuda")
+    out = md.moe_grouped_matmul(ones((R, K), "mxfp8"), offsets_of([R]), ones((1, N, K), wformat),
+                                w_s[None, :, None].expand(1, N, K // 32).contiguous(),
+                                a_s=a_s[:, None].expand(R, K // 32).contiguous(), wformat=wformat)
+    two = K * torch.exp2(a_s.double()[:, None] + w_s.double() - 254)
+    # the sum is K times a power of two: exact in float32 (54 + 64 gives subnormal values, which stay), and K = 96 .. 1152
+    # in bfloat16 too, unless subnormal
+    ref = two.float().to(torch.bfloat16)
+    nan = (a_s == 255)[:, None] | (w_s == 255)
+    assert torch.equal(out.isnan(), nan)
+    assert torch.equal(out[~nan], ref[~nan])
+
+
+@pytest.mark.parametrize("wformat", ["mxfp8", "mxfp4"])
+def test_scaled_product_nan(wformat):
+    """One NaN code or scale makes the outputs that it enters NaN and leaves the others; in an MXFP8 output a block
+    with a NaN has scale 255 and NaN codes."""
+    g = gen(17)
+    K, N, R = 640, 64, 70
+    a, a_s = whole_mx(g, (R, K), "mxfp8")
+    w = whole_mx(g, (1, N, K), wformat)
+    u = whole_mx(g, (1, N, K), wformat)
+    off = offsets_of([R])
+    good = md.moe_grouped_matmul(a, off, *w, a_s=a_s, wformat=wformat)
+    gq, gs = md.moe_grouped_gate_up(a, off, *w, *u, a_s=a_s, quantize=True, wformat=wformat)
+    a_s[3, 7] = 255
+    a[40, 600] = 0x7F
+    a[69, 0] = 0xFF
+    w[1][0, 5, 19] = 255
+    rows, cols = [3, 40, 69], [5]
+    if wformat == "mxfp8":
+        w[0][0, 33, 130] = 0x7F
+        cols.append(33)
+    nan = torch.zeros(R, N, dtype=torch.bool, device="cuda")
+    nan[rows] = True
+    nan[:, cols] = True
+    out = md.moe_grouped_matmul(a, off, *w, a_s=a_s, wformat=wformat)
+    assert torch.equal(out.isnan(), nan) and torch.equal(out[~nan], good[~nan])
+    q, s = md.moe_grouped_gate_up(a, off, *w, *u, a_s=a_s, quantize=True, wformat=wformat)
+    blocks = nan.unflatten(1, (-1, 32)).any(2)
+    assert torch.equal(s == 255, blocks)
+    assert torch.equal(q == 0x7F, blocks.repeat_interleave(32, 1))
+    assert torch.equal(s[~blocks], gs[~blocks])
+    keep = ~blocks.repeat_interleave(32, 1)
+    assert torch.equal(q[keep], gq[keep])
+
+
+@pytest.mark.parametrize("K", [512, 2048, 7168])
+@pytest.mark.parametrize("wformat", ["mxfp8", "mxfp4"])
+def test_scaled_product_error(K, wformat):
+    """The stated 2-norm of what is dropped. Four digits of minus the product, met by rows that are 1 in one place,
+    leave little but the error in the output, so that its bfloat16 rounding hides nothing."""
+    g = gen(K)
+    R, N = 32, 96
+
+    def encode(v):
+        if wformat == "mxfp8":
+            return quantize(v)
+        amax = v.unflatten(-1, (-1, 32)).abs().amax(-1)
+        s = (torch.frexp(amax)[1] - 3 + 127).to(torch.uint8)
+        t = torch.ldexp(v.unflatten(-1, (-1, 32)), (127 - s.int())[..., None]).flatten(-2)
+        table = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6], device="cuda")
+        c = (t.abs()[..., None] - table).abs().argmin(-1) + torch.where(t < 0, 8, 0)
+        return (c[..., 0::2] | (c[..., 1::2] << 4)).to(torch.uint8), s
+
+    a, a_s = random_mx(g, (R, K), "mxfp8")
+    w, w_s = random_mx(g, (N, K), wformat, 0.02)
+    main = decode(a, a_s) @ decode(w, w_s, wformat).T
+    rest, codes, scales = -main, [], []
+    for _ in range(4):
+        c, s = encode(rest.T.float().contiguous())
+        rest = rest - decode(c, s, wformat).T
+        codes.append(c)
+        scales.append(s)
+    places = torch.eye(32, device="cuda").repeat(1, 4)
+    p, p_s = quantize(places)
+    rows, row_s = torch.cat([a, p], 1), torch.cat([a_s, p_s], 1)
+    wq, ws = torch.cat([w, *codes], 1)[None].contiguous(), torch.cat([w_s, *scales], 1)[None].contiguous()
+    ref = decode(rows, row_s) @ decode(wq, ws, wformat)[0].T
+    out = md.moe_grouped_matmul(rows, offsets_of([R]), wq, ws, a_s=row_s, wformat=wformat)
+    err = float((out.double() - ref).norm() / main.norm())
+    print(f"scaled product {wformat} K={K}: {err:.2e} of the product's 2-norm", flush=True)
+    # the remainder's own rounding
+    assert float(ref.norm() / main.norm()) < 1e-3
+    assert err <= 2 * DROPPED + 2.0 ** -8 * float(ref.norm() / main.norm())
+
+
+@pytest.mark.parametrize("counts", ["few", "mid", "large", "some"])
+@pytest.mark.parametrize("wformat", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("K,N", [(2048, 96), (768, 512), (1056, 160)])
+def test_scaled_outputs_lie_next_to_the_exact_ones(counts, wformat, K, N):
+    counts = COUNTS[counts]
+    E, R = len(counts), sum(counts)
+    g = gen(K + N + R)
+    a, a_s = random_mx(g, (R, K), "mxfp8")
+    wg, wu = random_mx(g, (E, N, K), wformat, 0.02), random_mx(g, (E, N, K), wformat, 0.02)
+    off = offsets_of(counts)
+    av = decode(a, a_s)
+
+    def product(w):
+        v = decode(*w, wformat)
+        y, mag = products64(av, off, v)
+        sq, _ = products64(av * av, off, v * v)
+        return y, 10 * DROPPED * sq.sqrt() + 2 * K * U * mag
+
+    gate, dg = product(wg)
+    out = md.moe_grouped_matmul(a, off, *wg, a_s=a_s, wformat=wformat)
+    lo, hi = (gate - dg).float().to(torch.bfloat16), (gate + dg).float().to(torch.bfloat16)
+    assert ((out >= lo) & (out <= hi)).all()
+    up, du = product(wu)
+    silu = gate * torch.sigmoid(gate)
+    y = silu * up
+    # SiLU' is at most 1.1; the SwiGLU itself as in the tests of exact gates
+    d = 1.1 * dg * (up.abs() + du) + silu.abs() * du + (1.5 * gate.abs() + 16) * 2 * U * y.abs()
+    q, s = md.moe_grouped_gate_up(a, off, *wg, *wu, a_s=a_s, quantize=True, wformat=wformat)
+    yb, db = y.unflatten(1, (-1, 32)), d.unflatten(1, (-1, 32))
+    low = quantize((yb.abs() - db).clamp(min=0).float().flatten(1))[1]
+    high = quantize((yb.abs() + db).float().flatten(1))[1]
+    assert ((s >= low) & (s <= high)).all()
+    two = torch.exp2(127 - s.double())[..., None]
+
+    def code(v):
+        return (v * two).clamp(-448, 448).float().to(torch.float8_e4m3fn).float().flatten(1)
+
+    v = q.view(torch.float8_e4m3fn).float()
+    assert ((v >= code(yb - db)) & (v <= code(yb + db))).all()
+    moved = float((v != code(yb)).float().mean())
+    print(f"gate_up {wformat} K={K} N={N} R={R}: {moved:.2e} of the codes take a neighbour", flush=True)
+
+
+@pytest.mark.parametrize("wformat", ["mxfp8", "mxfp4"])
+def test_scaled_results_repeat(wformat):
+    """Bits of an MXFP8 layer of many tiles, call after call and through another tile list."""
+    g = gen(23)
+    E, K, N, R = 24, 768, 512, 5000
+    a, a_s = random_mx(g, (R, K), "mxfp8")
+    wg, wu = random_mx(g, (E, N, K), wformat, 0.02), random_mx(g, (E, N, K), wformat, 0.02)
+    cuts = torch.randint(0, R + 1, (E - 1,), generator=g, device="cuda").sort().values
+    off = torch.cat([cuts.new_zeros(1), cuts, cuts.new_full((1,), R)]).to(torch.int32)
+    first = md.moe_grouped_gate_up(a, off, *wg, *wu, a_s=a_s, quantize=True, wformat=wformat)
+    down = md.moe_grouped_matmul(a, off, *wg, a_s=a_s, wformat=wformat)
+    for _ in range(4):
+        again = md.moe_grouped_gate_up(a, off, *wg, *wu, a_s=a_s, quantize=True, wformat=wformat)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+        assert torch.equal(down, md.moe_grouped_matmul(a, off, *wg, a_s=a_s, wformat=wformat))
