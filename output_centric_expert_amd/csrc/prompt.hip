@@ -179,7 +179,8 @@ int moe_group(const int32_t* topk_ids, int B, int k, int E, int32_t* order, int3
 
 size_t moe_grouped_workspace_bytes(int E, int K, int N, int n_a, int a_rows, int matrices)
 {
-    if (check_product(a_rows, MOED_MXFP8, n_a, 1, true, 0, E, K, N) || (matrices != 1 && matrices != 2))
+    // sizes as without an order, whose limits are the wider ones
+    if (check_product(a_rows, MOED_MXFP8, n_a, 1, false, 0, E, K, N) || (matrices != 1 && matrices != 2))
         return 0;
     return moed::product_scales_bytes(E, K, N, n_a, a_rows == MOED_ROWS_MXFP8, matrices == 2);
 }

@@ -1,0 +1,25 @@
+"""Host-side checks of the prompt-side calls at the ends of their ranges (no GPU needed; the addresses are never
+read)."""
+import pytest
+
+from output_centric_expert_amd import moedecode as md
+from test_abi import A, lib  # noqa: F401
+from test_abi_prompt import matmul
+
+
+@pytest.mark.parametrize("rows,K,below,above", [(md.MOED_ROWS_BF16, 2880, 700_000, 800_000),
+                                                (md.MOED_ROWS_MXFP8, 1056, 4_000_000, 4_100_000)])
+def test_workspace_of_rows_in_place_past_4_gib(lib, rows, K, below, above):  # noqa: F811
+    """Without an order rows may take 4 GiB and more, and the workspace query answers for them too."""
+    size = 2 if rows == md.MOED_ROWS_BF16 else 1
+    assert below * K * size < 1 << 32 <= above * K * size
+    row = (K // 32 + 15) // 16 * 16
+    for n_a in (below, above):
+        for matrices in (1, 2):
+            need = lib.moe_grouped_workspace_bytes(8, K, 64, n_a, rows, matrices)
+            assert need == (8 * 64 * matrices + (n_a if rows == md.MOED_ROWS_MXFP8 else 0)) * row, n_a
+    kw = {"rows": rows, "a_s": A if rows == md.MOED_ROWS_MXFP8 else None, "n_a": above, "K": K}
+    need = lib.moe_grouped_workspace_bytes(8, K, 64, above, rows, 1)
+    assert matmul(lib, order=None, R=above, wsp=A, wsb=need - 1, **kw) == md.MOED_ERR_WORKSPACE
+    # gathered rows of that size are refused
+    assert matmul(lib, R=16, **kw) == md.MOED_ERR_SHAPE

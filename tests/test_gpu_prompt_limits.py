@@ -185,3 +185,27 @@ def test_scaled_results_repeat(wformat):
         again = md.moe_grouped_gate_up(a, off, *wg, *wu, a_s=a_s, quantize=True, wformat=wformat)
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
         assert torch.equal(down, md.moe_grouped_matmul(a, off, *wg, a_s=a_s, wformat=wformat))
+
+
+# ---------------------------------------------------------------------------- sizes
+
+@pytest.mark.parametrize("act,K,R", [("bf16", 2880, 800_000), ("mxfp8", 1056, 4_100_000)])
+def test_rows_in_place_past_4_gib_with_padded_scales(act, K, R):
+    """Rows in place beyond 2^32 bytes whose K needs its scales copied to the workspace."""
+    g = gen(K)
+    N, some = 32, 500
+    wq, ws = whole_mx(g, (2, N, K), "mxfp8")
+    off = torch.tensor([0, R - some, R], dtype=torch.int32, device="cuda")
+    if act == "bf16":
+        a, a_s = torch.zeros((R, K), dtype=torch.bfloat16, device="cuda"), None
+        a[-some:] = torch.randint(-4, 5, (some, K), generator=g, device="cuda").to(torch.bfloat16)
+        tail = a[-some:].double()
+    else:
+        a = torch.zeros((R, K), dtype=torch.uint8, device="cuda")
+        a_s = torch.full((R, K // 32), 127, dtype=torch.uint8, device="cuda")
+        a[-some:], a_s[-some:] = whole_mx(g, (some, K), "mxfp8")
+        tail = decode(a[-some:], a_s[-some:])
+    assert a.numel() * a.element_size() > 2 ** 32
+    out = md.moe_grouped_matmul(a, off, wq, ws, a_s=a_s)
+    assert torch.equal(out[-some:], (tail @ decode(wq, ws)[1].T).float().to(torch.bfloat16))
+    assert (out[:-some] == 0).all()
