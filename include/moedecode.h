@@ -347,7 +347,8 @@ typedef enum {
  * codes are y / 2^(scale-127) saturated to +-448 and rounded to nearest even;
  * a block that holds an infinity or a NaN gets scale 255 and NaN codes.
  * The squares are summed in float32: a row whose sum passes its range (values
- * from about 1e19) has y = 0.
+ * from about 1e19) has y = 0. Rows of any smaller size are exact to rounding,
+ * subnormal ones too; a row of zeros with eps = 0 is 0 / 0: NaN.
  * Limits (MOED_ERR_SHAPE): 1 <= H <= 32768, eps >= 0; H a multiple of 32 with
  * out_q. Pointers of x, residual, gain, residual_out, out and out_q are
  * 16-byte aligned (MOED_ERR_ALIGN). B = 0 launches nothing.

@@ -73,8 +73,32 @@ __device__ __forceinline__ void store_vals(void* p, size_t at, const float (&v)[
     }
 }
 
-// RES: 0 no residual, 1 bfloat16, 2 float32.
-template <int V, int NV, int TPR, bool XBF16, int RES>
+// Squares of a row whose sum is below 2^-80 (all |s| < 2^-40) may underflow, and its reciprocal root may pass
+// float32's range. With an eps as small (TINY) the row is then taken times 2^100, and eps times 2^200, which changes
+// nothing else: values from the smallest subnormal number to 2^60, their squares from 2^-98 to 2^120. Above, what is
+// lost to underflow is at most 2^15 squares below 2^-126 each: 2^-31 of the sum, or of eps. A kernel of its own, because
+// the test costs the others: a token of 2048 2.19 instead of 2.10 us, 8192 tokens of 2049 112.7 instead of 110.1.
+constexpr float kSmall = 0x1p-80f, kLift = 0x1p100f;
+
+// Sum over the threads of a row (one wavefront, or all of the workgroup), in every one of them.
+template <int W>
+__device__ __forceinline__ float row_sum(float v, float* part)
+{
+    v = wave_sum(v);
+    if constexpr (W > 1) {
+        if (threadIdx.x % kWave == 0)
+            part[threadIdx.x / kWave] = v;
+        __syncthreads();
+        v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+            v += part[w];
+    }
+    return v;
+}
+
+// RES: 0 no residual, 1 bfloat16, 2 float32. TINY: eps < kSmall.
+template <int V, int NV, int TPR, bool XBF16, int RES, bool TINY>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
 moe_norm_kernel(NormArgs p)
 {
@@ -110,18 +134,25 @@ moe_norm_kernel(NormArgs p)
 #pragma unroll
         for (int v = 0; v < V; ++v)
             ss = __builtin_fmaf(s[i][v], s[i][v], ss);
-    ss = wave_sum(ss);
-    if constexpr (kWaves > 1) {
-        __shared__ float part[kWaves];
-        if (t % kWave == 0)
-            part[t / kWave] = ss;
-        __syncthreads();
-        ss = 0.0f;
+    __shared__ float part[kWaves];
+    ss = row_sum<kWaves>(ss, part);
+    float eps = p.eps, mul = 1.0f;
+    if constexpr (TINY) {
+        if (ss < kSmall) {                                    // the same for all threads of a row
+            mul = kLift;
+            eps = eps * kLift * kLift;
+            ss = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w)
-            ss += part[w];
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    ss = __builtin_fmaf(s[i][v] * kLift, s[i][v] * kLift, ss);
+            if constexpr (kWaves > 1)
+                __syncthreads();                              // everybody has the first sum
+            ss = row_sum<kWaves>(ss, part);
+        }
     }
-    const float scale = rsqrtf(ss / (float)p.H + p.eps);
+    const float scale = rsqrtf(ss / (float)p.H + eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int h = (t + i * TPR) * V;
@@ -138,7 +169,7 @@ moe_norm_kernel(NormArgs p)
         float y[V];
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            y[v] = s[i][v] * scale * g[v];
+            y[v] = (TINY ? s[i][v] * mul : s[i][v]) * scale * g[v];
         if (p.out) {
             if (p.out_bf16)
                 store_vals<true>(p.out, row + h, y);
@@ -166,12 +197,12 @@ moe_norm_kernel(NormArgs p)
     }
 }
 
-template <int V, int NV, int TPR>
-hipError_t launch_shape(const NormArgs& p, bool x_bf16, int res, hipStream_t s)
+template <int V, int NV, int TPR, bool TINY>
+hipError_t launch_kind(const NormArgs& p, bool x_bf16, int res, hipStream_t s)
 {
     constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
     const dim3 grid((unsigned)((p.B + kRows - 1) / kRows)), block(TPR < 256 ? 256 : TPR);
-#define MOED_NORM(X, R) hipLaunchKernelGGL((moe_norm_kernel<V, NV, TPR, X, R>), grid, block, 0, s, p)
+#define MOED_NORM(X, R) hipLaunchKernelGGL((moe_norm_kernel<V, NV, TPR, X, R, TINY>), grid, block, 0, s, p)
     if (x_bf16) {
         if (res == 0) MOED_NORM(true, 0);
         else if (res == 1) MOED_NORM(true, 1);
@@ -183,6 +214,12 @@ hipError_t launch_shape(const NormArgs& p, bool x_bf16, int res, hipStream_t s)
     }
 #undef MOED_NORM
     return hipGetLastError();
+}
+
+template <int V, int NV, int TPR>
+hipError_t launch_shape(const NormArgs& p, bool x_bf16, int res, hipStream_t s)
+{
+    return p.eps < kSmall ? launch_kind<V, NV, TPR, true>(p, x_bf16, res, s) : launch_kind<V, NV, TPR, false>(p, x_bf16, res, s);
 }
 
 }  // namespace

@@ -209,3 +209,48 @@ def test_rows_in_place_past_4_gib_with_padded_scales(act, K, R):
     out = md.moe_grouped_matmul(a, off, wq, ws, a_s=a_s)
     assert torch.equal(out[-some:], (tail @ decode(wq, ws)[1].T).float().to(torch.bfloat16))
     assert (out[:-some] == 0).all()
+
+
+# ---------------------------------------------------------------------------- norm of tiny rows
+
+@pytest.mark.parametrize("B,H", [(3, 96), (2500, 96), (2, 31), (3, 2048), (2, 4104), (1, 8200), (1, 32768), (1, 32767)])
+@pytest.mark.parametrize("x_dtype,r_dtype", [(torch.float32, torch.float32), (torch.bfloat16, None),
+                                             (torch.bfloat16, torch.bfloat16)])
+def test_norm_of_tiny_rows(B, H, x_dtype, r_dtype):
+    """Rows whose squares leave float32's range below, with an eps that does not hide it."""
+    g = gen(B + H)
+    # below 2^-149 / 2^-133 a value is 0 already; 2^-39 and 2^-41 lie on both sides of where squares get small
+    for size in (1e-44, 1e-38, 1e-25, 1e-21, 2.0 ** -41, 2.0 ** -39):
+        x = (torch.randn(B, H, generator=g, device="cuda", dtype=torch.float64) * size).to(x_dtype)
+        x[:, 0] = size                            # no row of zeros
+        if H > 40:
+            x[0, 5:9] = 0.0
+        r = None if r_dtype is None else (torch.randn(B, H, generator=g, device="cuda", dtype=torch.float64) * size).to(r_dtype)
+        gain = 1 + 0.3 * torch.randn(H, generator=g, device="cuda")
+        s = (x.cpu().float() if r is None else x.cpu().float() + r.cpu().float()).cuda().double()
+        quant = H % 32 == 0
+        for eps in (0.0, 1e-42, 1e-30, 1e-25, 1e-20):
+            out, res, q, sc = md.moe_norm(x, gain, residual=r, eps=eps, out_dtype=torch.float32, quantize=quant)
+            e = float(torch.tensor(eps, dtype=torch.float32))
+            root = torch.sqrt((s * s).mean(1, keepdim=True) + e)
+            s_ok = (root > 0).expand_as(s)        # a row may have rounded, or cancelled, to zeros
+            y = s / root * gain.double()
+            # the row's sum of squares, root and products as for other rows; below 2^-126 values have absolute steps
+            tol = (H / 2 + 10) * U * y.abs() + 2.0 ** -148
+            assert ((out.double() - y).abs() <= tol)[s_ok].all(), (size, eps)
+            if r is not None:
+                assert torch.equal(res.double(), s.float().to(r_dtype).double())
+            if quant:
+                rq, rs = quantize(out)
+                assert torch.equal(sc, rs) and torch.equal(q, rq)
+
+
+def test_norm_of_a_row_of_zeros():
+    """0 / sqrt(eps), and 0 / 0 without an eps."""
+    x = torch.zeros(2, 64, device="cuda")
+    x[1] = 1e-30
+    gain = torch.ones(64, device="cuda")
+    out, _, q, s = md.moe_norm(x, gain, eps=0.0, out_dtype=torch.float32, quantize=True)
+    assert out[0].isnan().all() and (s[0] == 255).all() and ((out[1] - 1).abs() <= 2.0 ** -22).all()
+    out, _, q, s = md.moe_norm(x, gain, eps=1e-45, out_dtype=torch.float32, quantize=True)
+    assert (out[0] == 0).all() and (s[0] == 0).all() and (q[0] == 0).all()
