@@ -349,6 +349,8 @@ typedef enum {
  * The squares are summed in float32: a row whose sum passes its range (values
  * from about 1e19) has y = 0. Rows of any smaller size are exact to rounding,
  * subnormal ones too; a row of zeros with eps = 0 is 0 / 0: NaN.
+ * Outputs overlap nothing else; out and residual_out are not the same
+ * (MOED_ERR_SHAPE).
  * Limits (MOED_ERR_SHAPE): 1 <= H <= 32768, eps >= 0; H a multiple of 32 with
  * out_q. Pointers of x, residual, gain, residual_out, out and out_q are
  * 16-byte aligned (MOED_ERR_ALIGN). B = 0 launches nothing.
@@ -394,8 +396,8 @@ int moe_group(const int32_t *topk_ids, int B, int k, int E, int32_t *order,
  *            matrices) bytes (matrices: 2 for gate_up, 1 for matmul), 16-byte
  *            aligned, for the scales in rows of a multiple of 16 bytes; NULL
  *            where that is 0 (K >= 512, a multiple of 128)
- * Rows from offsets[E] on stay as they were. out may not overlap a. Limits
- * (MOED_ERR_SHAPE): K and N positive multiples of 32, below 2^20, K*N below
+ * Rows from offsets[E] on stay as they were. Outputs may not overlap inputs.
+ * Limits (MOED_ERR_SHAPE): K and N positive multiples of 32, below 2^20, K*N below
  * 2^32; E <= 2048; R and n_a below 2^28; (R/16 + E)*N/32 below 2^31; with an
  * order, `a` below 4 GiB; k >= 1. a, out and the code pointers are 16-byte
  * aligned, scales 4-byte (MOED_ERR_ALIGN). R = 0 launches nothing.
@@ -417,9 +419,9 @@ size_t moe_grouped_workspace_bytes(int E, int K, int N, int n_a, int a_rows, int
 /*
  * out[b][h] = sum_j topk_w[b][j] * y[position[b][j]][h], j in increasing order
  * in one float32 accumulator. y [R][H] y_dtype; out [B][H] out_dtype. A position
- * outside [0, R) makes the token's outputs NaN. Limits (MOED_ERR_SHAPE):
- * 1 <= k <= 64, 1 <= H < 2^20, R below 2^28. y and out are 16-byte aligned
- * (MOED_ERR_ALIGN). B = 0 launches nothing.
+ * outside [0, R) makes the token's outputs NaN. out may not overlap y. Limits
+ * (MOED_ERR_SHAPE): 1 <= k <= 64, 1 <= H < 2^20, R below 2^28. y and out are
+ * 16-byte aligned (MOED_ERR_ALIGN). B = 0 launches nothing.
  */
 int moe_combine(const void *y, int y_dtype, int R, const int32_t *position,
                 const float *topk_w, void *out, int out_dtype, int B, int k, int H,

@@ -144,6 +144,8 @@ int moe_norm(const void* x, int x_dtype, const void* residual, int residual_dtyp
     if (!aligned16(x) || !aligned16(residual) || !aligned16(gain) || !aligned16(residual_out) || !aligned16(out) ||
         !aligned16(out_q))
         return MOED_ERR_ALIGN;
+    if (out && out == residual_out)                           // the sum would be lost
+        return MOED_ERR_SHAPE;
     moed::NormArgs p;
     p.x = x; p.residual = residual; p.gain = gain; p.residual_out = residual_out; p.out = out;
     p.q = out_q; p.q_s = out_s;

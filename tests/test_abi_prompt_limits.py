@@ -4,7 +4,7 @@ import pytest
 
 from output_centric_expert_amd import moedecode as md
 from test_abi import A, lib  # noqa: F401
-from test_abi_prompt import matmul
+from test_abi_prompt import matmul, norm
 
 
 @pytest.mark.parametrize("rows,K,below,above", [(md.MOED_ROWS_BF16, 2880, 700_000, 800_000),
@@ -23,3 +23,9 @@ def test_workspace_of_rows_in_place_past_4_gib(lib, rows, K, below, above):  # n
     assert matmul(lib, order=None, R=above, wsp=A, wsb=need - 1, **kw) == md.MOED_ERR_WORKSPACE
     # gathered rows of that size are refused
     assert matmul(lib, R=16, **kw) == md.MOED_ERR_SHAPE
+
+
+def test_norm_refuses_one_buffer_for_two_outputs(lib):  # noqa: F811
+    """Both `out` and `residual_out` may be x or the residual, but not the same one."""
+    assert norm(lib) == md.MOED_ERR_SHAPE
+    assert norm(lib, B=0) == md.MOED_OK
