@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "launch.h"
+#include "lds_limits.h"
 #include "mx_device.h"
 
 namespace moed {
@@ -44,36 +45,23 @@ hipError_t check_flag(uint32_t** flag)
 
 hipError_t set_max_dynamic_lds(const void* func, int bytes)
 {
-    struct Entry {
-        int dev;
-        const void* func;
-        int bytes;
-    };
-    constexpr int kSlots = 256;                   // (device, kernel) pairs: a handful of kernels per device
+    static_assert(LdsLimits::kDevices == kMaxDevices, "one size per device");
     static std::mutex mu;
-    static Entry done[kSlots];
-    static int used = 0;
+    static LdsLimits limits;
     int dev = 0;
     hipError_t err = hipGetDevice(&dev);
     if (err != hipSuccess)
         return err;
+    if (dev < 0 || dev >= kMaxDevices)
+        return hipErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(mu);
-    int slot = -1;
-    for (int i = 0; i < used; ++i) {
-        if (done[i].dev == dev && done[i].func == func) {
-            if (done[i].bytes >= bytes)
-                return hipSuccess;
-            slot = i;
-        }
-    }
+    int* have = limits.find(func, dev);
+    if (have && *have >= bytes)
+        return hipSuccess;
     err = hipFuncSetAttribute(func, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (err != hipSuccess)
-        return err;
-    if (slot < 0 && used < kSlots)
-        slot = used++;
-    if (slot >= 0)
-        done[slot] = Entry{dev, func, bytes};
-    return hipSuccess;
+    if (err == hipSuccess && have)
+        *have = bytes;
+    return err;
 }
 
 __global__ void moe_check_clear_kernel(uint32_t* flag)

@@ -1,5 +1,9 @@
 """Host-side checks of the prompt-side calls at the ends of their ranges (no GPU needed; the addresses are never
 read)."""
+import os
+import re
+import subprocess
+
 import pytest
 
 from output_centric_expert_amd import moedecode as md
@@ -29,3 +33,43 @@ def test_norm_refuses_one_buffer_for_two_outputs(lib):  # noqa: F811
     """Both `out` and `residual_out` may be x or the residual, but not the same one."""
     assert norm(lib) == md.MOED_ERR_SHAPE
     assert norm(lib, B=0) == md.MOED_OK
+
+
+LIMITS = r"""
+#include <cstdio>
+#include "lds_limits.h"
+static moed::LdsLimits t;
+static char kernels[N + 1];
+int main()
+{
+    for (int d = 0; d < moed::LdsLimits::kDevices; ++d)
+        for (int k = 0; k < N; ++k) {
+            int* have = t.find(&kernels[k], d);
+            if (!have || *have)
+                return printf("kernel %d on device %d: %s\n", k, d, have ? "not new" : "no room");
+            *have = 1 + k * 100 + d;
+        }
+    for (int d = 0; d < moed::LdsLimits::kDevices; ++d)
+        for (int k = 0; k < N; ++k) {
+            int* have = t.find(&kernels[k], d);
+            if (!have || *have != 1 + k * 100 + d)
+                return printf("kernel %d on device %d is forgotten\n", k, d);
+        }
+    return N == moed::LdsLimits::kKernels && t.find(&kernels[N], 0) ? printf("more than all\n") : 0;
+}
+"""
+
+
+def test_lds_limits_of_every_kernel_on_every_device(lib, tmp_path):  # noqa: F811
+    """The table of LDS sizes holds each kernel that asks for one, on each device."""
+    names = subprocess.run(["nm", "-C", md.LIB_PATH], capture_output=True, text=True, check=True).stdout
+    asking = len(re.findall(r"__device_stub__(?:moe_product_tiled|moe_group_place|moe_gate_up_grouped_wide|"
+                            r"moe_down_expert)_kernel", names))
+    assert 0 < asking < 256
+    csrc = os.path.join(os.path.dirname(md.LIB_PATH), "csrc")
+    for n in (asking, 256):
+        src, exe = tmp_path / "limits.cpp", tmp_path / "limits"
+        src.write_text(LIMITS)
+        subprocess.run(["g++", "-std=c++17", f"-DN={n}", "-I", csrc, str(src), "-o", str(exe)], check=True)
+        done = subprocess.run([str(exe)], capture_output=True, text=True)
+        assert done.returncode == 0, done.stdout
