@@ -7,11 +7,15 @@ namespace moed {
 namespace {
 
 // Copies rows of n bytes to rows of `padded` bytes (a multiple of 16, the rest
-// zero: scale codes of values that do not exist), 16 bytes a thread. Bound by
-// memory: 1/32 of the codes' bytes once in and once out.
+// zero: scale codes of values that do not exist), 16 bytes a thread: the scales
+// of all experts' weight rows (N an expert in each matrix), then of the
+// activations' rows. K/32 bytes a row in and up to 16 times that out (K = 32).
+// With offsets, experts without rows are left out. An expert has rows only if
+// its offsets rise, whatever they are (build_tiles clamps them and takes the
+// largest so far), so what the others' places hold is never read.
 __global__ void __launch_bounds__(256)
 moe_pad_scales_kernel(const uint8_t* f0, const uint8_t* f1, const uint8_t* f2, uint8_t* t0, uint8_t* t1, uint8_t* t2,
-                      long long r0, long long r1, long long r2, int n, int padded)
+                      long long r0, long long r1, long long r2, int n, int padded, const int32_t* offsets, int N)
 {
     const int per = padded / 16;
     const long long all = (r0 + r1 + r2) * per;
@@ -24,10 +28,17 @@ moe_pad_scales_kernel(const uint8_t* f0, const uint8_t* f1, const uint8_t* f2, u
             row -= r0 + r1;
             from = f2;
             to = t2;
-        } else if (row >= r0) {
-            row -= r0;
-            from = f1;
-            to = t1;
+        } else {
+            if (row >= r0) {
+                row -= r0;
+                from = f1;
+                to = t1;
+            }
+            if (offsets) {
+                const int e = (int)(row / N);
+                if (offsets[e + 1] <= offsets[e])
+                    continue;
+            }
         }
         from += (size_t)row * n + c;
         u32x4 v{0, 0, 0, 0};
@@ -67,8 +78,13 @@ hipError_t launch_product(ProductArgs p, void* scales, hipStream_t s)
         uint8_t* ta = tu + (size_t)u * p.s_row;
         const long long all = (w + u + a) * (p.s_row / 16);
         const unsigned grid = (unsigned)((all + 255) / 256 < 4096 ? (all + 255) / 256 : 4096);
+        // Where many experts may be without rows (fewer than four an expert on average) those are left out; where few
+        // are, asking costs more. E = 128, 8 of them a token, K = 2880, N = 1120, gate and up in MXFP8: 8 tokens 88.8
+        // instead of 98.2 us, 1000 tokens 261.7 instead of 258.1; one token of one of 256 experts, K = 1056, N = 2048:
+        // 15.2 instead of 20.7.
+        const int32_t* offsets = p.R < 4LL * p.E ? p.offsets : nullptr;
         hipLaunchKernelGGL(moe_pad_scales_kernel, dim3(grid), dim3(256), 0, s, p.w_s, p.u_s, p.a_s, to, tu, ta, w, u, a,
-                           p.K / 32, p.s_row);
+                           p.K / 32, p.s_row, offsets, p.N);
         if (hipError_t e = hipGetLastError())
             return e;
         p.w_s = to;

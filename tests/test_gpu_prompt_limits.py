@@ -254,3 +254,31 @@ def test_norm_of_a_row_of_zeros():
     assert out[0].isnan().all() and (s[0] == 255).all() and ((out[1] - 1).abs() <= 2.0 ** -22).all()
     out, _, q, s = md.moe_norm(x, gain, eps=1e-45, out_dtype=torch.float32, quantize=True)
     assert (out[0] == 0).all() and (s[0] == 0).all() and (q[0] == 0).all()
+
+
+# ---------------------------------------------------------------------------- padded scales
+
+@pytest.mark.parametrize("offsets", [[0, 0, 3, 3, 3, 9, 9], [0, 7, 5, 9, 2, 2, 9], [4, -2, 1, 30, 2, 9, 9]])
+def test_padded_scales_of_experts_with_rows_only(offsets):
+    """Where scales are copied to the workspace, experts without rows are left out; offsets that make no sense still
+    give every row that a tile computes its scales."""
+    g = gen(11)
+    E, K, N, R = 6, 96, 64, 9
+    a = torch.randint(-4, 5, (R, K), generator=g, device="cuda").to(torch.bfloat16)
+    w, u = whole_mx(g, (E, N, K), "mxfp8"), whole_mx(g, (E, N, K), "mxfp8")
+    off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    # what a tile list makes of them: clamped to the rows, and rising
+    rising = np.maximum.accumulate(np.clip(offsets, 0, R))
+    ws = torch.full((md.moe_grouped_workspace_bytes(E, K, N, R, matrices=2),), 0x5A, dtype=torch.uint8, device="cuda")
+    md.moe_grouped_gate_up(a, off, *w, *u, workspace=ws)
+    copied = (ws.view(2, E, N * 16) != 0x5A).any(2).cpu().numpy()
+    rows = rising[1:] > rising[:-1]
+    asked = np.array(offsets[1:]) > np.array(offsets[:-1])
+    assert not (rows & ~asked).any()
+    assert (copied == asked).all()
+    ws = torch.full((md.moe_grouped_workspace_bytes(E, K, N, R),), 0x5A, dtype=torch.uint8, device="cuda")
+    out = md.moe_grouped_matmul(a, off, *w, out_dtype=torch.float32, workspace=ws)
+    wv = decode(*w)
+    for e in range(E):
+        some = slice(int(rising[e]), int(rising[e + 1]))
+        assert torch.equal(out[some], (a[some].double() @ wv[e].T).float())
