@@ -32,22 +32,22 @@ static __device__ const u32x4 kZeros = {0, 0, 0, 0};   // source of the values b
 // writes base + 16 i (base uniform). No register receives the data; the caller
 // waits on vmcnt before a barrier. Written as asm because the compiler makes
 // every later LDS read wait for the builtin's load, whatever buffer it fills.
-// (m0 is set by each; nothing else in these kernels uses it.)
 // The address is a uniform base plus a lane's 32-bit offset.
 __device__ __forceinline__ void load_to_lds16(const uint8_t* from, uint32_t offset, uint32_t base)
 {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(from), "s"(base) : "memory");
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(from), "s"(base)
+                 : "memory", "m0");
 }
 
 // The same from an address of each lane's own.
 __device__ __forceinline__ void load_to_lds16(const uint8_t* from, uint32_t base)
 {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(base) : "memory");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(base) : "memory", "m0");
 }
 
 __device__ __forceinline__ void load_to_lds4(const void* from, uint32_t base)
 {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(from), "s"(base) : "memory");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(from), "s"(base) : "memory", "m0");
 }
 
 template <int ROWS, bool FP4, int OUT, int RT, int NT, int WR, int WN>
