@@ -102,17 +102,9 @@ __device__ __forceinline__ int tile_expert(const int* first, int E, int tile)
     return __builtin_amdgcn_readfirstlane(e);
 }
 
-// Slot of sorted row r (r itself without an order), and the row of `a` that a
-// slot reads: slot / k, -1 where that lies outside.
-__device__ __forceinline__ int slot_of(const ProductArgs& p, int r)
-{
-    return p.order ? p.order[r] : r;
-}
-
+// Row of `a` that a slot of an order reads: slot / k, -1 where that lies outside.
 __device__ __forceinline__ int source_row(const ProductArgs& p, int slot)
 {
-    if (!p.order)
-        return slot;
     // slot / k by the reciprocal 2^32 / k, off by at most one
     int q = (int)__umulhi((unsigned)slot, p.inv_k);
     const int rest = slot - q * p.k;
