@@ -14,7 +14,8 @@
 // launches: the blocks' counts to the workspace, then every block adds up the
 // counts itself (blocks*E words out of L2, all threads at once where E <= 512:
 // 16384 tokens of 8 of 128 experts take 8.8 us, 20.8 us with one thread an
-// expert), which costs less than a launch in between would.
+// expert). Past kGroupScan blocks a launch in between scans the counts, so that
+// the time grows with the slots.
 #include "mx_device.h"
 #include "prompt.h"
 
@@ -24,6 +25,11 @@ namespace {
 
 constexpr int kGroupThreads = 1024;
 constexpr int kGroupWavesN = kGroupThreads / kWave;
+// Past this many blocks their counts are scanned in a launch of its own. Adding them up in every block grows with the
+// square of their number: 2^24 slots, 2048 blocks, take 447 us with 128 experts and 1780 with 2048 that way, 160 and 248
+// with the scan; at 256 blocks (2^21 slots) both take about the same (8 experts 18.7 and 19.9, 128 experts 28.8 and
+// 28.4, 2048 experts 66 and 45), and below the scan's launch is the larger part (2^17 slots of 128 experts 9.6 and 12.2).
+constexpr int kGroupScan = 256;
 
 // Lanes of the wavefront that hold the same id (ids < 2^bits), among `live`.
 __device__ __forceinline__ unsigned long long same_id(int id, int bits, unsigned long long live)
@@ -98,11 +104,44 @@ moe_group_count_kernel(const int32_t* ids, int n, int E, int32_t* counts)
         counts[(size_t)blockIdx.x * E + e] = hist[e];
 }
 
-// nblk = 1: counts unused. LDS: E ints (starts), then 16*E uint16 (per-wavefront counts).
+// counts[block][E] -> slots of the blocks before each (in place), and all blocks' sum in row nblk. A workgroup takes up
+// to 64 experts; its threads share the blocks in `parts` runs, whose sums meet in LDS.
+__global__ void __launch_bounds__(kGroupThreads)
+moe_group_scan_kernel(int32_t* counts, int E, int nblk)
+{
+    __shared__ int sums[kGroupThreads];
+    const int columns = E < kWave ? E : kWave, parts = kGroupThreads / columns;
+    const int q = threadIdx.x / columns, c = threadIdx.x % columns, e = blockIdx.x * columns + c;
+    const int per = (nblk + parts - 1) / parts;
+    const int from = q * per < nblk ? q * per : nblk, to = from + per < nblk ? from + per : nblk;
+    const bool live = q < parts && e < E;
+    int sum = 0;
+    if (live)
+#pragma unroll 8
+        for (int b = from; b < to; ++b)
+            sum += counts[(size_t)b * E + e];
+    sums[threadIdx.x] = sum;
+    __syncthreads();
+    if (!live)
+        return;                                   // no barrier follows
+    int at = 0;
+    for (int i = 0; i < q; ++i)
+        at += sums[i * columns + c];
+    if (q == parts - 1)
+        counts[(size_t)nblk * E + e] = at + sum;
+#pragma unroll 8
+    for (int b = from; b < to; ++b) {
+        const int n = counts[(size_t)b * E + e];
+        counts[(size_t)b * E + e] = at;
+        at += n;
+    }
+}
+
+// nblk = 1: counts unused. scanned: counts are those of the scan. LDS: E ints (starts), then 16*E uint16 (per-wavefront counts).
 template <int PER>
 __global__ void __launch_bounds__(kGroupThreads)
-moe_group_place_kernel(const int32_t* ids, int n, int E, int bits, int nblk, const int32_t* counts, int32_t* order,
-                       int32_t* position, int32_t* offsets)
+moe_group_place_kernel(const int32_t* ids, int n, int E, int bits, int nblk, bool scanned, const int32_t* counts,
+                       int32_t* order, int32_t* position, int32_t* offsets)
 {
     extern __shared__ int start[];                // E: first place of this block's slots of each expert
     uint16_t* cnt = reinterpret_cast<uint16_t*>(start + E);    // [16][E]
@@ -139,7 +178,7 @@ moe_group_place_kernel(const int32_t* ids, int n, int E, int bits, int nblk, con
     }
     __syncthreads();
     // few experts: the blocks' counts are added by parts = 1024 / E threads an expert
-    const int parts = nblk > 1 && E < kGroupThreads ? kGroupThreads / E : 1;
+    const int parts = nblk > 1 && !scanned && E < kGroupThreads ? kGroupThreads / E : 1;
     if (parts > 1) {
         const int q = tid / E, e = tid - q * E;
         if (q < parts) {
@@ -165,6 +204,9 @@ moe_group_place_kernel(const int32_t* ids, int n, int E, int bits, int nblk, con
             }
             if (nblk == 1) {
                 all = mine;
+            } else if (scanned) {
+                earlier = counts[(size_t)blk * E + e];
+                all = counts[(size_t)nblk * E + e];
             } else if (parts == 1) {
                 add_counts(counts, e, E, 0, nblk, blk, earlier, all);
             } else {                              // E <= 512: summed above by all threads
@@ -206,8 +248,8 @@ size_t group_workspace(int n, int E)
 {
     if (n <= kGroupOneBlock)
         return 0;
-    const size_t per = n <= (1 << 18) ? 2 : 8;
-    return ((size_t)n + per * kGroupThreads - 1) / (per * kGroupThreads) * (size_t)E * 4u;
+    const size_t per = n <= (1 << 18) ? 2 : 8, nblk = ((size_t)n + per * kGroupThreads - 1) / (per * kGroupThreads);
+    return (nblk + (nblk > kGroupScan ? 1 : 0)) * (size_t)E * 4u;
 }
 
 template <int PER>
@@ -228,8 +270,15 @@ static hipError_t launch_place(const int32_t* ids, int n, int E, int nblk, int32
         if (hipError_t e = hipGetLastError())
             return e;
     }
+    const bool scanned = nblk > kGroupScan;
+    if (scanned) {
+        hipLaunchKernelGGL(moe_group_scan_kernel, dim3((unsigned)(E + kWave - 1) / kWave), dim3(kGroupThreads), 0, s, counts,
+                           E, nblk);
+        if (hipError_t e = hipGetLastError())
+            return e;
+    }
     hipLaunchKernelGGL((moe_group_place_kernel<PER>), dim3((unsigned)nblk), dim3(kGroupThreads), lds, s, ids, n, E, bits,
-                       nblk, counts, order, position, offsets);
+                       nblk, scanned, counts, order, position, offsets);
     return hipGetLastError();
 }
 

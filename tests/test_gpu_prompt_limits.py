@@ -282,3 +282,65 @@ def test_padded_scales_of_experts_with_rows_only(offsets):
     for e in range(E):
         some = slice(int(rising[e]), int(rising[e + 1]))
         assert torch.equal(out[some], (a[some].double() @ wv[e].T).float())
+
+
+# ---------------------------------------------------------------------------- long lists of slots
+
+@pytest.mark.parametrize("B,k,E", [(262144, 8, 5), (262145, 8, 5), (300000, 8, 1), (300000, 8, 300), (65537, 64, 63),
+                                   (300001, 7, 64), (300001, 7, 65), (300000, 8, 1700), (2400000, 1, 2048)])
+@pytest.mark.parametrize("bad", [False, True])
+def test_group_of_many_slots(B, k, E, bad):
+    ids = torch.randint(-2 if bad else 0, E + (3 if bad else 0), (B, k), generator=gen(B + k + E), device="cuda",
+                        dtype=torch.int32)
+    order, position, offsets = md.moe_group(ids, E)
+    flat = ids.reshape(-1).cpu().numpy()
+    ok = np.flatnonzero((flat >= 0) & (flat < E))
+    ref = ok[np.argsort(flat[ok], kind="stable")]
+    pos = np.full(flat.size, -1)
+    pos[ref] = np.arange(ref.size)
+    assert np.array_equal(offsets.cpu().numpy(), np.concatenate([[0], np.cumsum(np.bincount(flat[ok], minlength=E))]))
+    assert np.array_equal(position.cpu().numpy().reshape(-1), pos)
+    assert np.array_equal(order.cpu().numpy(), np.concatenate([ref, np.full(flat.size - ref.size, -1)]))
+
+
+@pytest.mark.parametrize("B", [20000, 300000])
+def test_group_captured_and_replayed(B):
+    """Lists of several blocks: the counts in the workspace are made anew by every replay."""
+    E = 128
+    ids = torch.randint(0, E, (B, 8), generator=gen(1), device="cuda", dtype=torch.int32)
+    ws = torch.full((int(md.load().moe_group_workspace_bytes(B, 8, E)),), 255, dtype=torch.uint8, device="cuda")
+    got = md.moe_group(ids, E, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = md.moe_group(ids, E, workspace=ws)
+    for i in range(3):
+        ids.copy_(torch.randint(0, E, (B, 8), generator=gen(60 + i), device="cuda", dtype=torch.int32))
+        want = md.moe_group(ids, E)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), i
+
+
+def test_group_time_grows_with_the_slots():
+    """Eight times the slots take about eight times as long, not the square of it."""
+    def best(B):
+        ids = torch.randint(0, 256, (B, 8), generator=gen(B), device="cuda", dtype=torch.int32)
+        out = md.moe_group(ids, 256)
+        ws = torch.empty(int(md.load().moe_group_workspace_bytes(B, 8, 256)), dtype=torch.uint8, device="cuda")
+        times = []
+        for _ in range(6):
+            start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            start.record()
+            for _ in range(3):
+                md.moe_group(ids, 256, order=out[0], position=out[1], offsets=out[2], workspace=ws)
+            end.record()
+            torch.cuda.synchronize()
+            times.append(start.elapsed_time(end) / 3)
+        return min(times)
+
+    small, large = best(1 << 19), best((1 << 22) - 1)
+    print(f"group: {small * 1e3:.0f} us and {large * 1e3:.0f} us", flush=True)
+    assert large <= 16 * small
