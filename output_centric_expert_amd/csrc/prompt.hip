@@ -299,6 +299,9 @@ int moe_prefill(const void* x, const uint8_t* x_s, int x_rows, const int32_t* to
                          mx ? ws + l.a_s : nullptr, x_rows, R, E, H, I),
             ws + l.scales, s)))
         return st;
+    // Rows in out_dtype: float32 rows under a bfloat16 output would spare each term of the sum one rounding (2^-8 of it at
+    // most, as much as the output's own) for twice the bytes between the product and the sum: with bfloat16 rows 901
+    // instead of 790 us at 8192 tokens (8 of 128 experts, H = 2048, I = 768, MXFP8).
     if (int st = moed::abi_status(moed::launch_product(
             product_args(ws + l.a, mx ? ws + l.a_s : nullptr, R, nullptr, 1, offsets, wd_q, wd_s, nullptr, nullptr,
                          weight_format, ws + l.y, nullptr, out_dtype, R, E, I, H),

@@ -535,7 +535,10 @@ def moe_prefill_workspace_bytes(B: int, E: int, k: int, H: int, I: int, quantize
 def moe_prefill(x, topk_ids, topk_w, wg_q, wg_s, wu_q, wu_s, wd_q, wd_s, x_s=None, out=None,
                 out_dtype=torch.bfloat16, workspace=None, stream=None, wformat="mxfp8"):
     """The whole layer for prompts: returns out [B, H]. x: bfloat16 [B, H], or MXFP8 codes uint8 with x_s
-    uint8 [B, H/32] (moe_norm's quantized output). Same layer as moe_decode, by the grouped products."""
+    uint8 [B, H/32] (moe_norm's quantized output). The layer of moe_decode by the grouped products, with two
+    more roundings: the intermediate is kept in the type of x (bfloat16 or MXFP8, never float32), and each
+    expert's row in out_dtype before the weighted sum (moe_decode sums in float32 and rounds once; so does
+    this call with out_dtype float32)."""
     dev = torch.cuda.current_device()
     xp, xsp, x_rows = _rows(x, x_s, "x", dev)
     B, H = x.shape

@@ -10,7 +10,8 @@ import pytest
 import torch
 
 from output_centric_expert_amd import moedecode as md
-from test_gpu_prompt import COUNTS, U, decode, gen, gpu, products64, quantize, random_mx, whole_mx  # noqa: F401
+from test_gpu_prompt import (COUNTS, U, decode, gen, gpu, layer_inputs, products64, quantize, random_mx,  # noqa: F401
+                             whole_mx)
 
 pytestmark = pytest.mark.gpu
 
@@ -344,3 +345,24 @@ def test_group_time_grows_with_the_slots():
     small, large = best(1 << 19), best((1 << 22) - 1)
     print(f"group: {small * 1e3:.0f} us and {large * 1e3:.0f} us", flush=True)
     assert large <= 16 * small
+
+
+# ---------------------------------------------------------------------------- the layer with bfloat16 outputs
+
+@pytest.mark.parametrize("wformat", ["mxfp8", "mxfp4"])
+def test_prefill_agrees_with_decode_in_bfloat16(wformat):
+    """moe_prefill rounds each expert's row to bfloat16 before the weighted sum, moe_decode does not: a term is off by
+    at most half a step of it. Intermediate values can differ by one step where a float32 sum lies next to a border
+    (2 * 2^-8 of the result in the 2-norm allowed, as for float32 outputs), and both outputs are rounded once."""
+    x, logits, mats = layer_inputs(200, 16, 4, 512, 256, wformat, 27)
+    x = x.to(torch.bfloat16)
+    ids, w = md.moe_route(logits, 4)
+    ref = md.moe_decode(x, ids, w, *mats, inter_dtype=torch.bfloat16, wformat=wformat).double()
+    out = md.moe_prefill(x, ids, w, *mats, wformat=wformat).double()
+    rows = torch.zeros_like(ref)
+    for j in range(4):                            # the terms, one at a time
+        alone = torch.zeros_like(w)
+        alone[:, j] = w[:, j]
+        rows += md.moe_prefill(x, ids, alone, *mats, out_dtype=torch.float32, wformat=wformat).double().abs()
+    half = 2.0 ** -8
+    assert float((out - ref).norm()) <= 2 * half * float(ref.norm()) + half * float(rows.norm() + 2 * ref.norm())
