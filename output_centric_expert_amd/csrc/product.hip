@@ -91,6 +91,10 @@ hipError_t launch_product(ProductArgs p, void* scales, hipStream_t s)
         p.u_s = p.u_s ? tu : nullptr;
         p.a_s = p.a_s ? ta : nullptr;
     }
+    // The kinds of rows choose their tile by the average of rows an expert; their tables are of gate_up, K = 2048, N =
+    // 768. The product of K = 768, N = 2048 was timed with every bound halved and doubled: within 10 % at most sizes, but
+    // tiles of 16 rows would take 23 instead of 32 us at 4 rows an expert, bfloat16 x MXFP4, and the next larger ones 29
+    // instead of 36 at 16, MXFP8 x MXFP4 with float32 outputs.
     const int experts = p.R < p.E ? p.R : p.E;
     const long long avg = ((long long)p.R + experts - 1) / experts;
     if (!p.a_s)

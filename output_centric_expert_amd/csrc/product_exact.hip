@@ -19,6 +19,8 @@ template <bool FP4, bool GLU>
 hipError_t by_rows(const ProductArgs& p, int avg, hipStream_t s)
 {
     if constexpr (FP4) {
+        // up to 32 rows in all: few tiles, so a short one is done sooner (two fragments of weights 13.5 us, four 18.0, at
+        // 8 rows; 32 rows 16.8 and 18.7, 128 rows 30.5 and 29.7)
         if (avg < 4 && p.R < 32)
             return launch_shape<kRowsMXExact, FP4, GLU, kOutF32, 1, 2, 1, 4>(p, avg, s);
         if (avg < 8)
