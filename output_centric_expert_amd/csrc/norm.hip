@@ -15,10 +15,11 @@
 // A row is read once and stays in registers between the two passes of the
 // formula (V values per load, NV loads per thread, TPR threads per row), so the
 // kernel moves each input and output byte once. It is bound by memory: 8192
-// tokens of 4096 values, residual and MXFP8 included, take 49.4 us (303 MB at
-// 6.1 TB/s; a 2 GiB copy reaches 6.35). Loads and stores are streaming (cached:
-// 58 us). A single token is bound by one load and one reduction (1.9 us in a
-// graph). With 8 values per thread an MX block is four neighbouring lanes,
+// tokens of 4096 values, residual and MXFP8 included, take 49-54 us from box to
+// box (303 MB at 5.6-6.1 TB/s; a 2 GiB copy reaches 6.2-6.35). Loads and stores
+// are streaming (cached: 58 us). A single token is bound by one load and one
+// reduction (2 us in a graph). Rows that are no multiple of 8 go by single
+// values: 8192 tokens of 2049 bf16 110 us, of 1111 25 us (1.0 and 2.2 TB/s). With 8 values per thread an MX block is four neighbouring lanes,
 // whose largest value is found with two DPP steps.
 #include "mx_encode.h"
 #include "prompt.h"
