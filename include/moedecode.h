@@ -311,23 +311,29 @@ int moed_bench_read_cfg(const void *src, size_t bytes, void *sink, size_t sink_b
  *  - BFLOAT16 rows: weights are decoded to BFLOAT16 with the block scale folded
  *    in, exact in the range of scale codes given at moe_decode(); products are
  *    exact.
- *  - MXFP8 rows, BFLOAT16 or MXFP8 outputs: codes and block scales (any) enter
- *    the scaled matrix instructions as stored. These drop, among the products
- *    of a few neighbouring k, what lies about 2^-20 below the largest: with
- *    normal values 1.5e-5 of the result in the 2-norm (MXFP4 weights: 4e-6),
- *    1/260 of a BFLOAT16 rounding. An output next to a border between two
- *    rounded values can take the neighbour (0.2 % of the MXFP8 codes).
- *  - MXFP8 rows, FLOAT32 outputs: rows and weights are both decoded to
- *    BFLOAT16, so the range of scale codes applies to both; these are the
- *    outputs to ask for where sums as good as float32's are needed.
+ *  - MXFP8 rows: rows and weights are both decoded to BFLOAT16, so that range
+ *    applies to both. BFLOAT16 and MXFP8 outputs take scale codes outside it
+ *    too: where a block that is not all zeros has one, its tile of the product
+ *    is computed as with MXFP8_FAST.
+ *  - MXFP8_FAST rows, BFLOAT16 or MXFP8 outputs: codes and block scales (any)
+ *    enter the scaled matrix instructions as stored, in about half the time
+ *    from 128 rows an expert on. These add the products of eight neighbouring k
+ *    (8i..8i+7) dropping what lies 2^-14 below the largest of them, and are as
+ *    good as float32 from there on. With normal values that is 1.5e-5 of the
+ *    result in the 2-norm (MXFP4 weights: 4e-6), 1/260 of a BFLOAT16 rounding;
+ *    an output next to a border between two rounded values can take the
+ *    neighbour (0.2 % of the MXFP8 codes). FLOAT32 outputs are the same as with
+ *    MXFP8 rows.
  * Results are deterministic; how rows are tiled goes by the call's sizes, so a
  * row's low bits can differ between calls of different sizes.
  */
 typedef enum {
     MOED_ROWS_BF16 = 0,      /* bfloat16                                         */
     MOED_ROWS_F32 = 1,       /* float32 (outputs only)                           */
-    MOED_ROWS_MXFP8 = 2      /* E4M3 codes and, in a tensor of their own, one
+    MOED_ROWS_MXFP8 = 2,     /* E4M3 codes and, in a tensor of their own, one
                                 UE8M0 scale per 32 of a row                      */
+    MOED_ROWS_MXFP8_FAST = 4 /* the same, on the scaled matrix instructions
+                                (inputs only)                                    */
 } moed_rows;
 
 /*
@@ -383,14 +389,14 @@ int moe_group(const int32_t *topk_ids, int B, int k, int E, int32_t *order,
  * order = NULL:
  *   gate_up: out[r][n] = SiLU(Wg^[e][n] . a) * (Wu^[e][n] . a)
  *   matmul:  out[r][n] = W^[e][n] . a
- *   a        [n_a][K] a_rows: MOED_ROWS_BF16, or MOED_ROWS_MXFP8 with a_s
- *            [n_a][K/32] (NULL for bfloat16)
+ *   a        [n_a][K] a_rows: MOED_ROWS_BF16, or MOED_ROWS_MXFP8 (or its FAST
+ *            form) with a_s [n_a][K/32] (NULL for bfloat16)
  *   order    [R] int32 or NULL (then n_a >= R); an entry outside [0, n_a*k)
  *            makes the row NaN
  *   offsets  [E+1] int32, non-decreasing, from 0 to at most R. Other values
  *            give wrong rows but no access outside the tensors
  *   w_q, w_s [E][N][K] codes ([E][N][K/2] for MOED_MXFP4), [E][N][K/32] scales
- *   out      [R][N] out_rows (gate_up: any moed_rows; matmul: BF16 or F32)
+ *   out      [R][N] out_rows (gate_up: BF16, F32 or MXFP8; matmul: BF16 or F32)
  *   out_s    [R][N/32] for MOED_ROWS_MXFP8 (the rule of moe_norm), else NULL
  *   workspace at least moe_grouped_workspace_bytes(E, K, N, n_a, a_rows,
  *            matrices) bytes (matrices: 2 for gate_up, 1 for matmul), 16-byte
@@ -430,8 +436,8 @@ int moe_combine(const void *y, int y_dtype, int R, const int32_t *position,
 /*
  * The whole layer for prompts: moe_group, moe_grouped_gate_up,
  * moe_grouped_matmul, moe_combine on `stream`. Arguments as moe_decode(),
- * besides: x [B][H] x_rows (MOED_ROWS_BF16, or MOED_ROWS_MXFP8 with x_s
- * [B][H/32]). The intermediate is kept in the type of x (MXFP8 stays MXFP8, by
+ * besides: x [B][H] x_rows (MOED_ROWS_BF16, or MOED_ROWS_MXFP8 or its FAST form,
+ * for both products, with x_s [B][H/32]). The intermediate is kept in the type of x (MXFP8 stays MXFP8, by
  * the rule of moe_norm), the experts' rows in out_dtype. Ids outside [0, E)
  * make the token's outputs NaN; MOED_CHECK works as for moe_decode(). Limits:
  * those of the four calls. workspace: at least moe_prefill_workspace_bytes(...)

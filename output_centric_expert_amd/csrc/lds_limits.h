@@ -8,7 +8,7 @@ namespace moed {
 
 // Fixed, so that entry points for callers that cannot allocate may use it. A
 // slot per kernel (hashed by address) with one size per device, so that the
-// number of devices does not fill it; the library has about 110 kernels that ask.
+// number of devices does not fill it; the library has about 130 kernels that ask.
 struct LdsLimits {
     static constexpr int kKernels = 256, kDevices = 64;
 

@@ -99,7 +99,9 @@ hipError_t launch_product(ProductArgs p, void* scales, hipStream_t s)
     const long long avg = ((long long)p.R + experts - 1) / experts;
     if (!p.a_s)
         return launch_product_bf16(p, (int)avg, s);
-    return p.out_kind == kOutF32 ? launch_product_exact(p, (int)avg, s) : launch_product_mx(p, (int)avg, s);
+    if (p.out_kind == kOutF32)
+        return launch_product_exact(p, (int)avg, s);
+    return p.fast ? launch_product_mx(p, (int)avg, s) : launch_product_rounded(p, (int)avg, s);
 }
 
 }  // namespace moed

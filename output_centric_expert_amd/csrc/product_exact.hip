@@ -1,5 +1,5 @@
 // Products of MXFP8 rows with float32 outputs: rows and weights are both decoded to bfloat16 with their block scales
-// folded in, because the scaled matrix instructions lose more than float32 (product_mx.hip). Products are exact and
+// folded in, because the scaled matrix instructions drop more than float32 does (product_mx.hip). Products are exact and
 // the sums as good as any order of float32 additions (about 1e-7 of the result's norm).
 #include "product_tiled.h"
 

@@ -26,6 +26,14 @@ constexpr int kRowsBF16 = 0;      // bfloat16 rows, weights decoded to bfloat16
 constexpr int kRowsMX = 1;        // MXFP8 rows and MX weights as stored, scaled matrix instructions
 constexpr int kRowsMXExact = 2;   // MXFP8 rows and weights both decoded to bfloat16
 
+// Block scales that the decode to bfloat16 holds exactly with any code (255 is NaN either way).
+template <bool FP4>
+__device__ __forceinline__ bool exact_scale(uint32_t c)
+{
+    constexpr uint32_t lo = FP4 ? kExactScaleLoFP4 : kExactScaleLoFP8, hi = FP4 ? kExactScaleHiFP4 : kExactScaleHiFP8;
+    return c - lo <= hi - lo || c == 255u;
+}
+
 static __device__ const u32x4 kZeros = {0, 0, 0, 0};   // source of the values behind the end of a row
 
 // 16 bytes per lane from global memory straight to LDS: lane i of the wavefront
@@ -138,11 +146,15 @@ moe_product_tiled_kernel(ProductArgs p, int nblk, int group_blocks, int contiguo
     constexpr int kNeurons = 16 * kOutFrags * WN;             // outputs of a tile
     constexpr int kScratchRow = S::scratch_row(kOutFrags);
     constexpr int kAhead = 1;
+    // rounded outputs of rows and weights decoded to bfloat16: a tile that meets a block scale which the decode does not
+    // hold exactly is computed once more, with the scaled instructions
+    constexpr bool kRedo = ROWS == kRowsMXExact && OUT != kOutF32;
     extern __shared__ __align__(16) uint8_t lds[];
     uint8_t* const bad = lds + S::bad_at(kOutFrags);          // [2][kBM]: rows without a source
     int* const first = reinterpret_cast<int*>(lds + S::lds(kOutFrags));           // tiles before each expert
     int* const begin = first + p.E + 1;                       // its first row
     __shared__ int wsum[S::kWaves];
+    __shared__ int redo[2];                                   // by the tile's parity
     const int tid = threadIdx.x, lane = tid % kWave;
     const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int g = lane / 16, col = lane % 16;
@@ -302,9 +314,10 @@ moe_product_tiled_kernel(ProductArgs p, int nblk, int group_blocks, int contiguo
     const int w0 = wn * NT * 16 * S::kWU * 16, r0 = wr * RT * 16 * S::kRU * 16;
     constexpr int kWFrag = 16 * S::kWU * 16, kRFrag = 16 * S::kRU * 16;      // bytes of a fragment
     f32x4 acc[RT][NT];
-    // One step's products for the first n fragments of rows. `release` is called once the step's weights and scales are
-    // in registers.
-    auto compute = [&](int st, auto n, auto release) {
+    bool strange = false;                                     // this lane met such a scale (kRedo)
+    // One step's products for the first n fragments of rows, with the scaled instructions or on bfloat16. `release` is
+    // called once the step's weights and scales are in registers.
+    auto compute = [&](int st, auto n, auto scaled, auto release) {
         constexpr int N = decltype(n)::value;
         const uint8_t* wb = lds + S::kWAt + (st & 1) * S::kWBytes + w0;
         const uint8_t* rb = lds + (st & 1) * S::kRowBytes + r0;
@@ -312,7 +325,7 @@ moe_product_tiled_kernel(ProductArgs p, int nblk, int group_blocks, int contiguo
         const uint8_t* sb = lds + S::kScaleAt + (chunk & 1) * S::kScaleBytes + (4 * st - scales_from(chunk)) + 16 * col + g;
         const uint8_t* wsb = sb + wn * NT * 256;
         const uint8_t* rsb = sb + (S::kBN + wr * RT * 16) * 16;
-        if constexpr (S::kMX) {
+        if constexpr (decltype(scaled)::value) {
             i32x8 wv[NT], av[kAhead + 1];
             int wsc[NT], asc[RT];
             const uint8_t* rlo = rb + unit_at<8>(col, g);
@@ -356,6 +369,7 @@ moe_product_tiled_kernel(ProductArgs p, int nblk, int group_blocks, int contiguo
             // lane group g multiplies the block 32g .. 32g+31 of the step, 8 values per instruction
             u32x4 wq[NT][FP4 ? 1 : 2];
             float wsc[NT], asc[ROWS == kRowsMXExact ? RT : 1];
+            bool outside = false;
 #pragma unroll
             for (int f = 0; f < NT; ++f) {
                 if constexpr (FP4) {
@@ -364,14 +378,43 @@ moe_product_tiled_kernel(ProductArgs p, int nblk, int group_blocks, int contiguo
                     wq[f][0] = lds16(wb + unit_at<8>(col, 2 * g) + f * kWFrag);
                     wq[f][1] = lds16(wb + unit_at<8>(col, 2 * g + 1) + f * kWFrag);
                 }
-                wsc[f] = ue8m0_to_f32(wsb[f * 256]);
+                const uint32_t c = wsb[f * 256];
+                wsc[f] = ue8m0_to_f32(c);
+                if constexpr (kRedo)
+                    outside |= !exact_scale<FP4>(c);
             }
             if constexpr (ROWS == kRowsMXExact) {
 #pragma unroll
-                for (int r = 0; r < RT; ++r)
-                    asc[r] = ue8m0_to_f32(rsb[r * 256]);
+                for (int r = 0; r < RT; ++r) {
+                    const uint32_t c = rsb[r * 256];
+                    asc[r] = ue8m0_to_f32(c);
+                    if constexpr (kRedo)
+                        outside |= r < N && !exact_scale<false>(c);
+                }
             }
             release();
+            if constexpr (kRedo) {
+                if (__any(outside)) {                         // rare; blocks of zeros decode exactly whatever their scale
+#pragma unroll
+                    for (int f = 0; f < NT; ++f) {
+                        uint32_t any = 0;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            any |= FP4 ? wq[f][0][i] & 0x77777777u : (wq[f][0][i] | wq[f][FP4 ? 0 : 1][i]) & 0x7F7F7F7Fu;
+                        strange |= any != 0 && !exact_scale<FP4>(wsb[f * 256]);
+                    }
+#pragma unroll
+                    for (int r = 0; r < N; ++r) {
+                        const u32x4 lo = lds16(rb + unit_at<8>(col, 2 * g) + r * kRFrag);
+                        const u32x4 hi = lds16(rb + unit_at<8>(col, 2 * g + 1) + r * kRFrag);
+                        uint32_t any = 0;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            any |= (lo[i] | hi[i]) & 0x7F7F7F7Fu;
+                        strange |= any != 0 && !exact_scale<false>(rsb[r * 256]);
+                    }
+                }
+            }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 bf16x8 wv[NT];
@@ -417,12 +460,15 @@ moe_product_tiled_kernel(ProductArgs p, int nblk, int group_blocks, int contiguo
         __syncthreads();                                      // everybody has this tile's slots
         if (next.live)
             fetch_slots(next);
+        // all steps of the tile; the first ones are on their way
+        auto run_steps = [&](auto scaled) {
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
+            for (int r = 0; r < RT; ++r)
 #pragma unroll
-            for (int f = 0; f < NT; ++f)
-                acc[r][f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (t.live) {
+                for (int f = 0; f < NT; ++f)
+                    acc[r][f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (!t.live)
+                return;
             // row fragments of this wavefront that hold rows
             row_parts<RT>((t.rows - t.m0 - wr * RT * 16 + 15) / 16, [&](auto n) {
                 for (int st = 0; st < steps; ++st) {
@@ -436,7 +482,7 @@ moe_product_tiled_kernel(ProductArgs p, int nblk, int group_blocks, int contiguo
                     __syncthreads();
                     if (st + 1 < steps)
                         stage_rows(st + 1);
-                    compute(st, n, [&] {
+                    compute(st, n, scaled, [&] {
                         __syncthreads();                          // everybody has the step's weights
                         if ((st & 3) == 2 && st + 2 < steps)
                             stage_scales(st / 4 + 1);
@@ -445,10 +491,27 @@ moe_product_tiled_kernel(ProductArgs p, int nblk, int group_blocks, int contiguo
                     });
                 }
             });
+        };
+        if constexpr (kRedo) {
+            strange = false;
+            if (tid == 0)
+                redo[parity] = 0;                             // read last two tiles ago
         }
+        run_steps(std::bool_constant<S::kMX>{});
+        if constexpr (kRedo)
+            if (__any(strange) && lane == 0)
+                redo[parity] = 1;
         // the next tile's first steps are on their way while this one is stored
         wait_loads<0>();                                      // its slots, where this tile had no steps to wait in
         __syncthreads();
+        if constexpr (kRedo) {
+            if (redo[parity]) {                               // the same for all
+                stage_first();
+                run_steps(std::true_type{});
+                wait_loads<0>();
+                __syncthreads();
+            }
+        }
         if (next.live) {
             point(next, parity ^ 1);
             stage_first();

@@ -57,6 +57,7 @@ struct ProductArgs {
     uint32_t inv_k;         // 2^32 / k (2^32 - 1 for k = 1)
     int s_row;              // bytes between rows of scales: a multiple of 4, at least 16
     bool fp4;               // weights are MXFP4
+    bool fast;              // MXFP8 rows, rounded outputs: on the scaled matrix instructions
     int out_kind;           // kOutBF16, kOutF32 or kOutMX8
 };
 // The kernels fetch block scales 16 bytes of a row at a time, from dword
@@ -69,5 +70,6 @@ hipError_t launch_product(ProductArgs p, void* scales, hipStream_t s);
 hipError_t launch_product_bf16(const ProductArgs& p, int avg, hipStream_t s);
 hipError_t launch_product_mx(const ProductArgs& p, int avg, hipStream_t s);
 hipError_t launch_product_exact(const ProductArgs& p, int avg, hipStream_t s);
+hipError_t launch_product_rounded(const ProductArgs& p, int avg, hipStream_t s);
 
 }  // namespace moed

@@ -9,6 +9,7 @@ namespace {
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 inline bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 inline bool dtype_ok(int d) { return d == MOED_BF16 || d == MOED_F32; }
+inline bool rows_ok(int r) { return r == MOED_ROWS_BF16 || r == MOED_ROWS_MXFP8 || r == MOED_ROWS_MXFP8_FAST; }
 inline bool wformat_ok(int f) { return f == MOED_MXFP8 || f == MOED_MXFP4; }
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
@@ -39,7 +40,7 @@ int check_product(int a_rows, int wfmt, int n_a, int k, bool ordered, int R, int
     // the kernels address one expert's matrix, and gathered rows, with 32-bit offsets
     if ((long long)K * N >= (1LL << 32) || (ordered && (long long)n_a * K * (a_rows == MOED_ROWS_BF16 ? 2 : 1) >= (1LL << 32)))
         return MOED_ERR_SHAPE;
-    if ((a_rows != MOED_ROWS_BF16 && a_rows != MOED_ROWS_MXFP8) || !wformat_ok(wfmt))
+    if (!rows_ok(a_rows) || !wformat_ok(wfmt))
         return MOED_ERR_DTYPE;
     return MOED_OK;
 }
@@ -56,7 +57,7 @@ int check_scales(size_t need, const void* workspace, size_t bytes)
     return aligned16(workspace) ? MOED_OK : MOED_ERR_ALIGN;
 }
 
-moed::ProductArgs product_args(const void* a, const uint8_t* a_s, int n_a, const int32_t* order, int k,
+moed::ProductArgs product_args(const void* a, const uint8_t* a_s, bool fast, int n_a, const int32_t* order, int k,
                                const int32_t* offsets, const uint8_t* w_q, const uint8_t* w_s, const uint8_t* u_q,
                                const uint8_t* u_s, int wfmt, void* out, uint8_t* out_s, int out_rows, int R, int E,
                                int K, int N)
@@ -70,6 +71,7 @@ moed::ProductArgs product_args(const void* a, const uint8_t* a_s, int n_a, const
     p.n_a = n_a; p.k = k; p.R = R; p.E = E; p.K = K; p.N = N;
     p.inv_k = (uint32_t)(k == 1 ? 0xFFFFFFFFu : (1ull << 32) / (unsigned)k);
     p.fp4 = wfmt == MOED_MXFP4;
+    p.fast = fast;
     p.out_kind = out_rows;
     return p;
 }
@@ -95,9 +97,9 @@ int prefill_layout(int B, int E, int k, int H, int I, int x_rows, int out_dtype,
         return MOED_ERR_SHAPE;
     if (H < 32 || I < 32 || H % 32 != 0 || I % 32 != 0 || H >= kMaxRowLength || I >= kMaxRowLength)
         return MOED_ERR_SHAPE;
-    if ((x_rows != MOED_ROWS_BF16 && x_rows != MOED_ROWS_MXFP8) || !dtype_ok(out_dtype))
+    if (!rows_ok(x_rows) || !dtype_ok(out_dtype))
         return MOED_ERR_DTYPE;
-    const bool mx = x_rows == MOED_ROWS_MXFP8;
+    const bool mx = x_rows != MOED_ROWS_BF16;
     if (too_many_tiles((long long)B * k, E, H > I ? H : I) || (long long)H * I >= (1LL << 32) ||
         (long long)B * H * (mx ? 1 : 2) >= (1LL << 32))
         return MOED_ERR_SHAPE;
@@ -184,7 +186,7 @@ size_t moe_grouped_workspace_bytes(int E, int K, int N, int n_a, int a_rows, int
     // sizes as without an order, whose limits are the wider ones
     if (check_product(a_rows, MOED_MXFP8, n_a, 1, false, 0, E, K, N) || (matrices != 1 && matrices != 2))
         return 0;
-    return moed::product_scales_bytes(E, K, N, n_a, a_rows == MOED_ROWS_MXFP8, matrices == 2);
+    return moed::product_scales_bytes(E, K, N, n_a, a_rows != MOED_ROWS_BF16, matrices == 2);
 }
 
 int moe_grouped_gate_up(const void* a, const uint8_t* a_s, int a_rows, int n_a, const int32_t* order, int k,
@@ -198,7 +200,7 @@ int moe_grouped_gate_up(const void* a, const uint8_t* a_s, int a_rows, int n_a, 
         return st;
     if (R == 0)
         return MOED_OK;
-    if (!a || !offsets || !wg_q || !wg_s || !wu_q || !wu_s || !out || (a_rows == MOED_ROWS_MXFP8) != (a_s != nullptr) ||
+    if (!a || !offsets || !wg_q || !wg_s || !wu_q || !wu_s || !out || (a_rows != MOED_ROWS_BF16) != (a_s != nullptr) ||
         (out_rows == MOED_ROWS_MXFP8) != (out_s != nullptr))
         return MOED_ERR_NULL;
     if (!aligned16(a) || !aligned16(wg_q) || !aligned16(wu_q) || !aligned16(out) || !aligned4(wg_s) || !aligned4(wu_s) ||
@@ -206,9 +208,10 @@ int moe_grouped_gate_up(const void* a, const uint8_t* a_s, int a_rows, int n_a, 
         return MOED_ERR_ALIGN;
     if (int st = check_scales(moed::product_scales_bytes(E, K, N, n_a, a_s != nullptr, true), workspace, workspace_bytes))
         return st;
-    return moed::abi_status(moed::launch_product(product_args(a, a_s, n_a, order, k, offsets, wg_q, wg_s, wu_q, wu_s,
-                                                        weight_format, out, out_s, out_rows, R, E, K, N),
-                                           workspace, static_cast<hipStream_t>(stream)));
+    return moed::abi_status(moed::launch_product(
+        product_args(a, a_s, a_rows == MOED_ROWS_MXFP8_FAST, n_a, order, k, offsets, wg_q, wg_s, wu_q, wu_s, weight_format,
+                     out, out_s, out_rows, R, E, K, N),
+        workspace, static_cast<hipStream_t>(stream)));
 }
 
 int moe_grouped_matmul(const void* a, const uint8_t* a_s, int a_rows, int n_a, const int32_t* order, int k,
@@ -221,15 +224,16 @@ int moe_grouped_matmul(const void* a, const uint8_t* a_s, int a_rows, int n_a, c
         return st;
     if (R == 0)
         return MOED_OK;
-    if (!a || !offsets || !w_q || !w_s || !out || (a_rows == MOED_ROWS_MXFP8) != (a_s != nullptr))
+    if (!a || !offsets || !w_q || !w_s || !out || (a_rows != MOED_ROWS_BF16) != (a_s != nullptr))
         return MOED_ERR_NULL;
     if (!aligned16(a) || !aligned16(w_q) || !aligned16(out) || !aligned4(w_s) || !aligned4(a_s))
         return MOED_ERR_ALIGN;
     if (int st = check_scales(moed::product_scales_bytes(E, K, N, n_a, a_s != nullptr, false), workspace, workspace_bytes))
         return st;
-    return moed::abi_status(moed::launch_product(product_args(a, a_s, n_a, order, k, offsets, w_q, w_s, nullptr, nullptr,
-                                                        weight_format, out, nullptr, out_rows, R, E, K, N),
-                                           workspace, static_cast<hipStream_t>(stream)));
+    return moed::abi_status(moed::launch_product(
+        product_args(a, a_s, a_rows == MOED_ROWS_MXFP8_FAST, n_a, order, k, offsets, w_q, w_s, nullptr, nullptr,
+                     weight_format, out, nullptr, out_rows, R, E, K, N),
+        workspace, static_cast<hipStream_t>(stream)));
 }
 
 int moe_combine(const void* y, int y_dtype, int R, const int32_t* position, const float* topk_w, void* out,
@@ -268,7 +272,7 @@ int moe_prefill(const void* x, const uint8_t* x_s, int x_rows, const int32_t* to
         return MOED_ERR_DTYPE;
     if (B == 0)
         return MOED_OK;
-    const bool mx = x_rows == MOED_ROWS_MXFP8;
+    const bool mx = x_rows != MOED_ROWS_BF16, fast = x_rows == MOED_ROWS_MXFP8_FAST;
     if (!x || mx != (x_s != nullptr) || !topk_ids || !topk_w || !wg_q || !wg_s || !wu_q || !wu_s || !wd_q || !wd_s ||
         !out || !workspace)
         return MOED_ERR_NULL;
@@ -279,7 +283,8 @@ int moe_prefill(const void* x, const uint8_t* x_s, int x_rows, const int32_t* to
         return MOED_ERR_ALIGN;
     hipStream_t s = static_cast<hipStream_t>(stream);
     // where weights are decoded to bfloat16 the block scales are folded into the conversion, as in the large-batch
-    // kernels: both steps with bfloat16 rows, the down step with float32 outputs
+    // kernels: both steps with bfloat16 rows, the down step with float32 outputs (MXFP8 rows with rounded outputs take
+    // any scale)
     moed::CheckArgs c;
     c.ids = topk_ids;
     c.wg_q = wg_q; c.wg_s = wg_s; c.wu_q = wu_q; c.wu_s = wu_s; c.wd_q = wd_q; c.wd_s = wd_s;
@@ -295,15 +300,15 @@ int moe_prefill(const void* x, const uint8_t* x_s, int x_rows, const int32_t* to
                                                offsets, s)))
         return st;
     if (int st = moed::abi_status(moed::launch_product(
-            product_args(x, x_s, B, order, k, offsets, wg_q, wg_s, wu_q, wu_s, weight_format, ws + l.a,
-                         mx ? ws + l.a_s : nullptr, x_rows, R, E, H, I),
+            product_args(x, x_s, fast, B, order, k, offsets, wg_q, wg_s, wu_q, wu_s, weight_format, ws + l.a,
+                         mx ? ws + l.a_s : nullptr, mx ? MOED_ROWS_MXFP8 : MOED_ROWS_BF16, R, E, H, I),
             ws + l.scales, s)))
         return st;
     // Rows in out_dtype: float32 rows under a bfloat16 output would spare each term of the sum one rounding (2^-8 of it at
     // most, as much as the output's own) for twice the bytes between the product and the sum: with bfloat16 rows 901
     // instead of 790 us at 8192 tokens (8 of 128 experts, H = 2048, I = 768, MXFP8).
     if (int st = moed::abi_status(moed::launch_product(
-            product_args(ws + l.a, mx ? ws + l.a_s : nullptr, R, nullptr, 1, offsets, wd_q, wd_s, nullptr, nullptr,
+            product_args(ws + l.a, mx ? ws + l.a_s : nullptr, fast, R, nullptr, 1, offsets, wd_q, wd_s, nullptr, nullptr,
                          weight_format, ws + l.y, nullptr, out_dtype, R, E, I, H),
             ws + l.scales, s)))
         return st;

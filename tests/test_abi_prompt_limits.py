@@ -8,7 +8,7 @@ import pytest
 
 from output_centric_expert_amd import moedecode as md
 from test_abi import A, lib  # noqa: F401
-from test_abi_prompt import matmul, norm
+from test_abi_prompt import gate_up, matmul, norm, prefill
 
 
 @pytest.mark.parametrize("rows,K,below,above", [(md.MOED_ROWS_BF16, 2880, 700_000, 800_000),
@@ -73,3 +73,21 @@ def test_lds_limits_of_every_kernel_on_every_device(lib, tmp_path):  # noqa: F81
         subprocess.run(["g++", "-std=c++17", f"-DN={n}", "-I", csrc, str(src), "-o", str(exe)], check=True)
         done = subprocess.run([str(exe)], capture_output=True, text=True)
         assert done.returncode == 0, done.stdout
+
+
+def test_fast_rows(lib):  # noqa: F811
+    """The fast form of MXFP8 rows is checked as MXFP8 rows are, and is no kind of output."""
+    fast = md.MOED_ROWS_MXFP8_FAST
+    for call in (gate_up, matmul):
+        assert call(lib, rows=fast) == md.MOED_ERR_NULL
+        assert call(lib, rows=fast, a_s=A, R=0) == md.MOED_OK
+        assert call(lib, rows=fast, a_s=A, K=64) == md.MOED_ERR_NULL
+        assert call(lib, out_rows=fast) == md.MOED_ERR_DTYPE
+    assert prefill(lib, rows=fast) == md.MOED_ERR_NULL
+    assert prefill(lib, rows=fast, x_s=A, wsb=16) == md.MOED_ERR_WORKSPACE
+    for args in ((8, 64, 32, 5), (8, 512, 32, 5), (4, 1120, 64, 1000)):
+        for two in (1, 2):
+            assert (lib.moe_grouped_workspace_bytes(*args, fast, two) ==
+                    lib.moe_grouped_workspace_bytes(*args, md.MOED_ROWS_MXFP8, two))
+    assert (lib.moe_prefill_workspace_bytes(2, 8, 2, 64, 32, fast, 1) ==
+            lib.moe_prefill_workspace_bytes(2, 8, 2, 64, 32, md.MOED_ROWS_MXFP8, 1) > 0)

@@ -1,9 +1,10 @@
-"""GPU tests of the prompt-side operators at the ends of their ranges: block scales of every size, NaN and the
-error of the scaled matrix instructions (MXFP8 rows with bfloat16 or MXFP8 outputs).
+"""GPU tests of the prompt-side operators at the ends of their ranges: the sums behind bfloat16 and MXFP8 outputs of
+MXFP8 rows, block scales of every size, NaN, tiny rows, long lists and large tensors.
 
-What those instructions drop measured 1.4e-5 to 1.5e-5 of the result in the 2-norm with normal values. It is a sum of
-many small parts, so a single output is held to ten times that, of the 2-norm of its own terms, and a 2-norm over
-thousands of outputs to twice that. Rounding keeps order, so an output whose unrounded value lies within d of the
+A float32 sum of K terms is off by at most 2^-23 a term of the sum of their magnitudes (test_gpu_prompt). What the
+scaled matrix instructions (fast) drop measured 1.4e-5 to 1.5e-5 of the result in the 2-norm with normal values. It is
+a sum of many small parts, so a single output is held to ten times that, of the 2-norm of its own terms, and a 2-norm
+over thousands of outputs to twice that. Rounding keeps order, so an output whose unrounded value lies within d of the
 exact y lies between the roundings of y - d and y + d."""
 import numpy as np
 import pytest
@@ -28,7 +29,94 @@ def offsets_of(counts):
     return torch.tensor([0] + list(np.cumsum(counts)), dtype=torch.int32, device="cuda")
 
 
-# ---------------------------------------------------------------------------- scaled matrix instructions
+# ---------------------------------------------------------------------------- sums of MXFP8 rows
+
+def eights(K, R):
+    """Rows with 256, -256 and six times 2^-6 in every eight values: sums that lose their small terms where an eight is
+    aligned to its largest."""
+    v = torch.full((R, K), 2.0 ** -6, device="cuda")
+    v[:, 0::8], v[:, 3::8] = 256.0, -256.0
+    return (v.to(torch.float8_e4m3fn).view(torch.uint8),
+            torch.full((R, K // 32), 127, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("rows", [1, 5, 20, 40, 100, 300])
+@pytest.mark.parametrize("wformat", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("K", [96, 512, 1152])
+def test_rounded_outputs_are_of_whole_sums(rows, wformat, K):
+    """Weights of 64: every product is a whole number and every sum below 2^24, exact in float32 in any order."""
+    N = 96
+    a, a_s = eights(K, rows)
+    w_q = ones((1, N, K), wformat)
+    w_s = torch.full((1, N, K // 32), 133, dtype=torch.uint8, device="cuda")
+    off = offsets_of([rows])
+    want = 6 * K // 8
+    out = md.moe_grouped_matmul(a, off, w_q, w_s, a_s=a_s, wformat=wformat)
+    assert (out == want).all()                    # 72, 384 and 864 are bfloat16 values
+    u_s = w_s - 3                                 # ups of an eighth
+    kw = {"a_s": a_s, "wformat": wformat}
+    y = md.moe_grouped_gate_up(a, off, w_q, w_s, w_q, u_s, out_dtype=torch.float32, **kw)
+    assert (y == want * want / 8).all()           # SiLU of 72 and more is its argument
+    assert torch.equal(md.moe_grouped_gate_up(a, off, w_q, w_s, w_q, u_s, **kw), y.to(torch.bfloat16))
+    q, s = md.moe_grouped_gate_up(a, off, w_q, w_s, w_q, u_s, quantize=True, **kw)
+    rq, rs = quantize(y)
+    assert torch.equal(q, rq) and torch.equal(s, rs)
+
+
+@pytest.mark.parametrize("wformat", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("counts", ["few", "mid", "large"])
+def test_scales_outside_the_exact_range(wformat, counts):
+    """Rows times 2^-123 in one block of 32 and 2^123 in another, weights the other way round: the same whole sums."""
+    counts = COUNTS[counts]
+    E, R, K, N = len(counts), sum(counts), 640, 96
+    g = gen(R)
+    a, a_s = whole_mx(g, (R, K), "mxfp8")
+    w_q, w_s = whole_mx(g, (E, N, K), wformat)
+    u_q, u_s = whole_mx(g, (E, N, K), wformat)
+    off = offsets_of(counts)
+    plain = md.moe_grouped_matmul(a, off, w_q, w_s, a_s=a_s, wformat=wformat)
+    q, s = md.moe_grouped_gate_up(a, off, w_q, w_s, u_q, u_s, a_s=a_s, quantize=True, wformat=wformat)
+    for block, by in ((4, 123), (19, -123)):
+        a_s[:, block] = (a_s[:, block].int() - by).to(torch.uint8)
+        w_s[:, :, block] = (w_s[:, :, block].int() + by).to(torch.uint8)
+        u_s[:, :, block] = (u_s[:, :, block].int() + by).to(torch.uint8)
+    assert torch.equal(md.moe_grouped_matmul(a, off, w_q, w_s, a_s=a_s, wformat=wformat), plain)
+    q2, s2 = md.moe_grouped_gate_up(a, off, w_q, w_s, u_q, u_s, a_s=a_s, quantize=True, wformat=wformat)
+    assert torch.equal(q, q2) and torch.equal(s, s2)
+
+
+@pytest.mark.parametrize("wformat", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("K", [256, 224])
+def test_scales_outside_the_exact_range_change_their_tiles_only(wformat, K):
+    """A block with such a scale makes its tile lose the small terms of its eights; other tiles keep theirs, and blocks
+    of zeros may have any scale."""
+    N, R = 256, 700
+    a, a_s = eights(K, R)
+    w_q = ones((2, N, K), wformat)
+    w_s = torch.full((2, N, K // 32), 133, dtype=torch.uint8, device="cuda")
+    off = torch.tensor([0, 350, R], dtype=torch.int32, device="cuda")
+    call = lambda: md.moe_grouped_matmul(a, off, w_q, w_s, a_s=a_s, wformat=wformat)  # noqa: E731
+    whole, block = 6 * K // 8, 24
+    assert (call() == whole).all()
+    a[690, 32:96] = 0
+    a_s[690, 1], a_s[690, 2] = 0, 254
+    w_q[1, 7, : w_q.shape[2] * 32 // K] = 0
+    w_s[1, 7, 0] = 1
+    want = torch.full((R, N), float(whole), device="cuda")
+    want[690] -= 2 * block
+    want[350:, 7] -= block
+    assert torch.equal(call().float(), want)
+    a_s[690, 5] = 3
+    out = call().float()
+    assert torch.equal(out[:350], want[:350])
+    lost = (out[350:] == 0) | (out[350:] == want[350:])
+    lost[340] = True
+    assert lost.all()
+    if wformat == "mxfp8":                        # the tile was computed with the scaled instructions
+        assert (out[691, 8:] == 0).all()
+
+
+# ---------------------------------------------------------------------------- every scale, NaN, error
 
 SCALES = (0, 1, 2, 10, 54, 60, 64, 100, 126, 127, 128, 150, 190, 245, 253, 254, 255)
 
@@ -36,7 +124,8 @@ SCALES = (0, 1, 2, 10, 54, 60, 64, 100, 126, 127, 128, 150, 190, 245, 253, 254, 
 @pytest.mark.parametrize("K", [96, 128, 512, 1152])
 @pytest.mark.parametrize("wformat", ["mxfp8", "mxfp4"])
 @pytest.mark.parametrize("rows_each", [1, 40])
-def test_scaled_product_takes_every_scale(K, wformat, rows_each):
+@pytest.mark.parametrize("fast", [False, True])
+def test_product_takes_every_scale(K, wformat, rows_each, fast):
     """Every pair of a row's and a weight's scale code: K * 2^(s + t - 254), NaN where either is 255."""
     a_s = torch.tensor(SCALES, dtype=torch.uint8, device="cuda").repeat_interleave(rows_each)
     R, N = a_s.numel(), 32
@@ -44,7 +133,7 @@ def test_scaled_product_takes_every_scale(K, wformat, rows_each):
     w_s[:len(SCALES)] = torch.tensor(SCALES, dtype=torch.uint8, device="cuda")
     out = md.moe_grouped_matmul(ones((R, K), "mxfp8"), offsets_of([R]), ones((1, N, K), wformat),
                                 w_s[None, :, None].expand(1, N, K // 32).contiguous(),
-                                a_s=a_s[:, None].expand(R, K // 32).contiguous(), wformat=wformat)
+                                a_s=a_s[:, None].expand(R, K // 32).contiguous(), wformat=wformat, fast=fast)
     two = K * torch.exp2(a_s.double()[:, None] + w_s.double() - 254)
     # the sum is K times a power of two: exact in float32 (54 + 64 gives subnormal values, which stay), and K = 96 .. 1152
     # in bfloat16 too, unless subnormal
@@ -55,7 +144,8 @@ def test_scaled_product_takes_every_scale(K, wformat, rows_each):
 
 
 @pytest.mark.parametrize("wformat", ["mxfp8", "mxfp4"])
-def test_scaled_product_nan(wformat):
+@pytest.mark.parametrize("fast", [False, True])
+def test_rounded_product_nan(wformat, fast):
     """One NaN code or scale makes the outputs that it enters NaN and leaves the others; in an MXFP8 output a block
     with a NaN has scale 255 and NaN codes."""
     g = gen(17)
@@ -64,8 +154,8 @@ def test_scaled_product_nan(wformat):
     w = whole_mx(g, (1, N, K), wformat)
     u = whole_mx(g, (1, N, K), wformat)
     off = offsets_of([R])
-    good = md.moe_grouped_matmul(a, off, *w, a_s=a_s, wformat=wformat)
-    gq, gs = md.moe_grouped_gate_up(a, off, *w, *u, a_s=a_s, quantize=True, wformat=wformat)
+    good = md.moe_grouped_matmul(a, off, *w, a_s=a_s, wformat=wformat, fast=fast)
+    gq, gs = md.moe_grouped_gate_up(a, off, *w, *u, a_s=a_s, quantize=True, wformat=wformat, fast=fast)
     a_s[3, 7] = 255
     a[40, 600] = 0x7F
     a[69, 0] = 0xFF
@@ -77,9 +167,9 @@ def test_scaled_product_nan(wformat):
     nan = torch.zeros(R, N, dtype=torch.bool, device="cuda")
     nan[rows] = True
     nan[:, cols] = True
-    out = md.moe_grouped_matmul(a, off, *w, a_s=a_s, wformat=wformat)
+    out = md.moe_grouped_matmul(a, off, *w, a_s=a_s, wformat=wformat, fast=fast)
     assert torch.equal(out.isnan(), nan) and torch.equal(out[~nan], good[~nan])
-    q, s = md.moe_grouped_gate_up(a, off, *w, *u, a_s=a_s, quantize=True, wformat=wformat)
+    q, s = md.moe_grouped_gate_up(a, off, *w, *u, a_s=a_s, quantize=True, wformat=wformat, fast=fast)
     blocks = nan.unflatten(1, (-1, 32)).any(2)
     assert torch.equal(s == 255, blocks)
     assert torch.equal(q == 0x7F, blocks.repeat_interleave(32, 1))
@@ -90,8 +180,9 @@ def test_scaled_product_nan(wformat):
 
 @pytest.mark.parametrize("K", [512, 2048, 7168])
 @pytest.mark.parametrize("wformat", ["mxfp8", "mxfp4"])
-def test_scaled_product_error(K, wformat):
-    """The stated 2-norm of what is dropped. Four digits of minus the product, met by rows that are 1 in one place,
+@pytest.mark.parametrize("fast", [False, True])
+def test_rounded_product_error(K, wformat, fast):
+    """Float32 sums behind rounded outputs, and the stated 2-norm of what fast drops. Four digits of minus the product, met by rows that are 1 in one place,
     leave little but the error in the output, so that its bfloat16 rounding hides nothing."""
     g = gen(K)
     R, N = 32, 96
@@ -120,18 +211,21 @@ def test_scaled_product_error(K, wformat):
     rows, row_s = torch.cat([a, p], 1), torch.cat([a_s, p_s], 1)
     wq, ws = torch.cat([w, *codes], 1)[None].contiguous(), torch.cat([w_s, *scales], 1)[None].contiguous()
     ref = decode(rows, row_s) @ decode(wq, ws, wformat)[0].T
-    out = md.moe_grouped_matmul(rows, offsets_of([R]), wq, ws, a_s=row_s, wformat=wformat)
+    out = md.moe_grouped_matmul(rows, offsets_of([R]), wq, ws, a_s=row_s, wformat=wformat, fast=fast)
     err = float((out.double() - ref).norm() / main.norm())
-    print(f"scaled product {wformat} K={K}: {err:.2e} of the product's 2-norm", flush=True)
-    # the remainder's own rounding
+    print(f"product {wformat} K={K} fast={fast}: {err:.2e} of the product's 2-norm", flush=True)
+    # the remainder's own rounding, and K roundings or truncations of independent sign of partial sums that are no larger
+    # than the product
     assert float(ref.norm() / main.norm()) < 1e-3
-    assert err <= 2 * DROPPED + 2.0 ** -8 * float(ref.norm() / main.norm())
+    tol = 2.0 ** -8 * float(ref.norm() / main.norm()) + 2 * (K + 128) ** 0.5 * U
+    assert err <= tol + (2 * DROPPED if fast else 0)
 
 
 @pytest.mark.parametrize("counts", ["few", "mid", "large", "some"])
 @pytest.mark.parametrize("wformat", ["mxfp8", "mxfp4"])
 @pytest.mark.parametrize("K,N", [(2048, 96), (768, 512), (1056, 160)])
-def test_scaled_outputs_lie_next_to_the_exact_ones(counts, wformat, K, N):
+@pytest.mark.parametrize("fast", [False, True])
+def test_rounded_outputs_lie_next_to_the_exact_ones(counts, wformat, K, N, fast):
     counts = COUNTS[counts]
     E, R = len(counts), sum(counts)
     g = gen(K + N + R)
@@ -144,10 +238,10 @@ def test_scaled_outputs_lie_next_to_the_exact_ones(counts, wformat, K, N):
         v = decode(*w, wformat)
         y, mag = products64(av, off, v)
         sq, _ = products64(av * av, off, v * v)
-        return y, 10 * DROPPED * sq.sqrt() + 2 * K * U * mag
+        return y, (10 * DROPPED * sq.sqrt() if fast else 0) + 2 * K * U * mag
 
     gate, dg = product(wg)
-    out = md.moe_grouped_matmul(a, off, *wg, a_s=a_s, wformat=wformat)
+    out = md.moe_grouped_matmul(a, off, *wg, a_s=a_s, wformat=wformat, fast=fast)
     lo, hi = (gate - dg).float().to(torch.bfloat16), (gate + dg).float().to(torch.bfloat16)
     assert ((out >= lo) & (out <= hi)).all()
     up, du = product(wu)
@@ -155,7 +249,7 @@ def test_scaled_outputs_lie_next_to_the_exact_ones(counts, wformat, K, N):
     y = silu * up
     # SiLU' is at most 1.1; the SwiGLU itself as in the tests of exact gates
     d = 1.1 * dg * (up.abs() + du) + silu.abs() * du + (1.5 * gate.abs() + 16) * 2 * U * y.abs()
-    q, s = md.moe_grouped_gate_up(a, off, *wg, *wu, a_s=a_s, quantize=True, wformat=wformat)
+    q, s = md.moe_grouped_gate_up(a, off, *wg, *wu, a_s=a_s, quantize=True, wformat=wformat, fast=fast)
     yb, db = y.unflatten(1, (-1, 32)), d.unflatten(1, (-1, 32))
     low = quantize((yb.abs() - db).clamp(min=0).float().flatten(1))[1]
     high = quantize((yb.abs() + db).float().flatten(1))[1]
@@ -168,11 +262,12 @@ def test_scaled_outputs_lie_next_to_the_exact_ones(counts, wformat, K, N):
     v = q.view(torch.float8_e4m3fn).float()
     assert ((v >= code(yb - db)) & (v <= code(yb + db))).all()
     moved = float((v != code(yb)).float().mean())
-    print(f"gate_up {wformat} K={K} N={N} R={R}: {moved:.2e} of the codes take a neighbour", flush=True)
+    print(f"gate_up {wformat} K={K} N={N} R={R} fast={fast}: {moved:.2e} of the codes take a neighbour", flush=True)
 
 
 @pytest.mark.parametrize("wformat", ["mxfp8", "mxfp4"])
-def test_scaled_results_repeat(wformat):
+@pytest.mark.parametrize("fast", [False, True])
+def test_rounded_results_repeat(wformat, fast):
     """Bits of an MXFP8 layer of many tiles, call after call and through another tile list."""
     g = gen(23)
     E, K, N, R = 24, 768, 512, 5000
@@ -180,12 +275,12 @@ def test_scaled_results_repeat(wformat):
     wg, wu = random_mx(g, (E, N, K), wformat, 0.02), random_mx(g, (E, N, K), wformat, 0.02)
     cuts = torch.randint(0, R + 1, (E - 1,), generator=g, device="cuda").sort().values
     off = torch.cat([cuts.new_zeros(1), cuts, cuts.new_full((1,), R)]).to(torch.int32)
-    first = md.moe_grouped_gate_up(a, off, *wg, *wu, a_s=a_s, quantize=True, wformat=wformat)
-    down = md.moe_grouped_matmul(a, off, *wg, a_s=a_s, wformat=wformat)
+    first = md.moe_grouped_gate_up(a, off, *wg, *wu, a_s=a_s, quantize=True, wformat=wformat, fast=fast)
+    down = md.moe_grouped_matmul(a, off, *wg, a_s=a_s, wformat=wformat, fast=fast)
     for _ in range(4):
-        again = md.moe_grouped_gate_up(a, off, *wg, *wu, a_s=a_s, quantize=True, wformat=wformat)
+        again = md.moe_grouped_gate_up(a, off, *wg, *wu, a_s=a_s, quantize=True, wformat=wformat, fast=fast)
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
-        assert torch.equal(down, md.moe_grouped_matmul(a, off, *wg, a_s=a_s, wformat=wformat))
+        assert torch.equal(down, md.moe_grouped_matmul(a, off, *wg, a_s=a_s, wformat=wformat, fast=fast))
 
 
 # ---------------------------------------------------------------------------- sizes
@@ -366,3 +461,53 @@ def test_prefill_agrees_with_decode_in_bfloat16(wformat):
         rows += md.moe_prefill(x, ids, alone, *mats, out_dtype=torch.float32, wformat=wformat).double().abs()
     half = 2.0 ** -8
     assert float((out - ref).norm()) <= 2 * half * float(ref.norm()) + half * float(rows.norm() + 2 * ref.norm())
+
+
+# ---------------------------------------------------------------------------- MXFP8 rows on the scaled instructions
+
+@pytest.mark.parametrize("wformat", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_prefill_fast(wformat, out_dtype):
+    """The layer of the default call: where an intermediate code takes its neighbour it is an eighth of it off (2 % of
+    the codes allowed: an eighth of the root of that), sums differ by what is dropped, bfloat16 rows and outputs by
+    their roundings."""
+    x, logits, mats = layer_inputs(700, 16, 4, 512, 256, wformat, 33)
+    q, s = quantize(x)
+    ids, w = md.moe_route(logits, 4)
+    ref = md.moe_prefill(q, ids, w, *mats, x_s=s, out_dtype=out_dtype, wformat=wformat).double()
+    out = md.moe_prefill(q, ids, w, *mats, x_s=s, out_dtype=out_dtype, wformat=wformat, fast=True).double()
+    rel = float((out - ref).norm() / ref.norm())
+    print(f"prefill fast {wformat} {out_dtype}: {rel:.2e}", flush=True)
+    assert 0 < rel <= 0.02 ** 0.5 / 8 + (3 * 2.0 ** -8 if out_dtype == torch.bfloat16 else 0)
+
+
+def test_prefill_fast_captured_and_replayed():
+    x, logits, mats = layer_inputs(600, 16, 4, 256, 128, "mxfp8", 31)
+    q, s = quantize(x)
+    ids, w = md.moe_route(logits, 4)
+    call = lambda fast: md.moe_prefill(q, ids, w, *mats, x_s=s, fast=fast)  # noqa: E731
+    call(True), call(False)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call(True), call(False)
+    for i in range(3):
+        a, b = quantize(torch.randn(600, 256, generator=gen(70 + i), device="cuda"))
+        q.copy_(a)
+        s.copy_(b)
+        want = call(True), call(False)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for u, v in zip(got, want):
+            assert torch.equal(u, v), i
+
+
+def test_fast_refusals():
+    a = torch.ones(4, 64, dtype=torch.bfloat16, device="cuda")
+    w_q, w_s = torch.zeros(2, 32, 64, dtype=torch.uint8, device="cuda"), torch.zeros(2, 32, 2, dtype=torch.uint8, device="cuda")
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="fast"):
+        md.moe_grouped_matmul(a, off, w_q, w_s, fast=True)
+    with pytest.raises(ValueError, match="fast"):
+        md.moe_grouped_gate_up(a, off, w_q, w_s, w_q, w_s, fast=True)
