@@ -5,11 +5,13 @@
 // weight rows, rows and block scales go from memory straight to LDS, two buffers of each; while a tile is stored, the
 // next one's first step is on its way. The mathematics is in product_common.h; what bounds a call:
 //  - up to about 50 rows an expert, the weights' bytes: 512 tokens of 8 of 128 experts, K = 2048, N = 768, gate and up
-//    in MXFP8 take 80 us with MXFP8 rows (5.3 TB/s of codes and scales), 83 us with bfloat16 rows;
-//  - beyond, the matrix instructions. With MXFP8 rows 8192 tokens take 280-288 us (1.43-1.47 PFLOP/s; the same loop
-//    without loads 224 us: the clock falls to 1.7 GHz under these instructions), of which the tiles' beginnings and ends
-//    are a sixth. With bfloat16 rows the decode of the weights (16 conversions for 4 * RT matrix instructions) comes on
-//    top.
+//    in MXFP8 take 83 us with bfloat16 rows (5.1 TB/s of codes and scales), 90 with MXFP8 rows decoded to it, 80 with
+//    MXFP8 rows on the scaled instructions;
+//  - beyond, the matrix instructions and what goes with them. On the scaled ones 8192 tokens take 280-288 us (1.43-1.47
+//    PFLOP/s; the same loop without loads 224 us: the clock falls to 1.7 GHz under these instructions), of which the
+//    tiles' beginnings and ends are a sixth. With bfloat16 rows (461-491 us) the decode of the weights (16 conversions
+//    for 4 * RT matrix instructions) comes on top, with MXFP8 rows decoded to it (522-540 us) also the rows' (16 for
+//    4 * NT, by every wavefront that reads them).
 // What did not pay: fragments of the weights read straight from memory (a load of 16 rows x 64 bytes runs at a quarter
 // of the rate of one of 8 rows x 128 bytes); two groups of wavefronts taking turns between LDS and the matrix unit, and
 // loads spread among the matrix instructions (both wait longer for the loads than they save).
