@@ -437,11 +437,12 @@ int moe_combine(const void *y, int y_dtype, int R, const int32_t *position,
  * The whole layer for prompts: moe_group, moe_grouped_gate_up,
  * moe_grouped_matmul, moe_combine on `stream`. Arguments as moe_decode(),
  * besides: x [B][H] x_rows (MOED_ROWS_BF16, or MOED_ROWS_MXFP8 or its FAST form,
- * for both products, with x_s [B][H/32]). The intermediate is kept in the type of x (MXFP8 stays MXFP8, by
- * the rule of moe_norm), the experts' rows in out_dtype. Ids outside [0, E)
- * make the token's outputs NaN; MOED_CHECK works as for moe_decode(). Limits:
- * those of the four calls. workspace: at least moe_prefill_workspace_bytes(...)
- * bytes (0 for invalid arguments), 16-byte aligned.
+ * for both products, with x_s [B][H/32]). The intermediate is kept in the type
+ * of x (MXFP8 stays MXFP8, by the rule of moe_norm), the experts' rows in
+ * out_dtype. Ids outside [0, E) make the token's outputs NaN; MOED_CHECK works
+ * as for moe_decode(). Limits: those of the four calls. workspace: at least
+ * moe_prefill_workspace_bytes(...) bytes (0 for invalid arguments), 16-byte
+ * aligned.
  */
 size_t moe_prefill_workspace_bytes(int B, int E, int k, int H, int I, int x_rows, int out_dtype);
 int moe_prefill(const void *x, const uint8_t *x_s, int x_rows, const int32_t *topk_ids,

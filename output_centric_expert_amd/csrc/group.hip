@@ -137,7 +137,8 @@ moe_group_scan_kernel(int32_t* counts, int E, int nblk)
     }
 }
 
-// nblk = 1: counts unused. scanned: counts are those of the scan. LDS: E ints (starts), then 16*E uint16 (per-wavefront counts).
+// nblk = 1: counts unused. scanned: counts are those of the scan. LDS: E ints (starts), then 16*E uint16 (per-wavefront
+// counts).
 template <int PER>
 __global__ void __launch_bounds__(kGroupThreads)
 moe_group_place_kernel(const int32_t* ids, int n, int E, int bits, int nblk, bool scanned, const int32_t* counts,

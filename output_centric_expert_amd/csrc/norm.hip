@@ -19,8 +19,9 @@
 // box (303 MB at 5.6-6.1 TB/s; a 2 GiB copy reaches 6.2-6.35). Loads and stores
 // are streaming (cached: 58 us). A single token is bound by one load and one
 // reduction (2 us in a graph). Rows that are no multiple of 8 go by single
-// values: 8192 tokens of 2049 bf16 110 us, of 1111 25 us (1.0 and 2.2 TB/s). With 8 values per thread an MX block is four neighbouring lanes,
-// whose largest value is found with two DPP steps.
+// values: 8192 tokens of 2049 bf16 110 us, of 1111 25 us (1.2 and 2.9 TB/s).
+// With 8 values per thread an MX block is four neighbouring lanes, whose
+// largest value is found with two DPP steps.
 #include "mx_encode.h"
 #include "prompt.h"
 
