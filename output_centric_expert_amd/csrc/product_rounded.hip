@@ -5,7 +5,8 @@
 //
 // A block scale outside the range that the decode holds exactly (10..245 of MXFP8, 2..252 of MXFP4; 255 is NaN either
 // way), of a block that is not all zeros, makes its tile be computed once more with the scaled instructions, which take
-// any scale.
+// any scale. Steps that hold such a scale look at the block's codes: 8192 tokens, half of them zeros with scale 0, take 664
+// us instead of 551 (gate_up below); with such a block in every second row, all tiles twice, 773.
 #include "product_tiled.h"
 
 namespace moed {
