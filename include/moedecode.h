@@ -452,6 +452,147 @@ int moe_prefill(const void *x, const uint8_t *x_s, int x_rows, const int32_t *to
                 void *out, int out_dtype, int B, int E, int k, int H, int I,
                 void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * The operators around the MoE block: the router's logits and other dense
+ * products, the router's choice by scores and groups, and what stands between
+ * a block's output and the next block. One layer's half is
+ *   moe_norm -> moe_linear -> moe_route_scored -> moe_decode or moe_prefill
+ *   -> moe_post_norm (which is the next block's moe_norm too).
+ * Inference operators like the rest: no gradients. The conventions at the top
+ * of this file hold; B is below 2^22.
+ */
+
+typedef enum {
+    MOED_ACT_NONE = 0,
+    MOED_ACT_SILU = 1,       /* v / (1 + exp(-v))                                */
+    MOED_ACT_GELU = 2,       /* v (1 + erf(v / sqrt 2)) / 2                      */
+    MOED_ACT_GELU_TANH = 3,  /* v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2  */
+    MOED_ACT_RELU = 4,       /* max(v, 0)                                        */
+    MOED_ACT_SIGMOID = 5,    /* 1 / (1 + exp(-v))                                */
+    MOED_ACT_TANH = 6
+} moed_activation;
+
+/*
+ * Dense product with an epilogue:
+ *   out[b][n] = act(sum_k x[b][k] w[n][k] + bias[n]) + residual[b][n]
+ *   x         [B][K] x_dtype (moed_dtype)
+ *   w         [N][K] w_dtype
+ *   bias      [N] bias_dtype, or NULL: 0
+ *   residual  [B][N] residual_dtype, or NULL: 0; may be out where the types
+ *             agree
+ *   out       [B][N] out_dtype, rounded once; overlaps nothing else
+ *   activation  a moed_activation
+ * K and N are any positive numbers (router logits: N experts; a shared
+ * expert's gate: N = 1). Sums are float32 of exact products; float32 operands
+ * keep float32 precision: above a few rows they enter the matrix instructions
+ * as three bfloat16 parts whose sum is the value (products of two float32
+ * values leave out the parts below 2^-23 of the product). Where x or w holds an
+ * infinity, a NaN or a float32 value that rounds to an infinite bfloat16
+ * (3.39e38 and more), the outputs that it enters are infinite or NaN.
+ * A row's low bits can differ between calls of different sizes.
+ * workspace: at least moe_linear_workspace_bytes(...) bytes (0 for invalid
+ * arguments), 16-byte aligned; NULL where that is 0.
+ * Limits (MOED_ERR_SHAPE): 1 <= K, N < 2^20; K*N below 2^32; B*K and B*N below
+ * 2^40. x, w, residual and out are 16-byte aligned, bias by its element
+ * (MOED_ERR_ALIGN). B = 0 launches nothing.
+ */
+size_t moe_linear_workspace_bytes(int B, int K, int N, int x_dtype, int w_dtype);
+int moe_linear(const void *x, int x_dtype, const void *w, int w_dtype,
+               const void *bias, int bias_dtype, int activation,
+               const void *residual, int residual_dtype, void *out, int out_dtype,
+               int B, int K, int N, void *workspace, size_t workspace_bytes, void *stream);
+
+typedef enum {
+    MOED_SCORE_SOFTMAX = 0,  /* s_e = exp(l_e - m) / sum_e' exp(l_e' - m)        */
+    MOED_SCORE_SIGMOID = 1   /* s_e = 1 / (1 + exp(-l_e))                        */
+} moed_score;
+
+typedef enum {
+    MOED_GROUP_MAX = 0,      /* a group is worth its largest choice              */
+    MOED_GROUP_TOP2 = 1      /* ... the sum of its two largest choices           */
+} moed_group_score;
+
+/*
+ * Router by scores, a bias for balance and groups of experts. Per token, from
+ * its logits l [E]:
+ *   scores  s_e as above, rounded once to float32
+ *   choice  c_e = s_e + bias[e] in float32 (bias NULL: s_e)
+ *   groups  the E experts form n_group groups of neighbours. With topk_group <
+ *           n_group only experts of the topk_group groups of the largest value
+ *           (of their choices, by group_score; a float32 sum) can be chosen
+ *   chosen  the k experts of the largest choice, in descending order
+ *   weights w_j = s_e(j), or with renormalize s_e(j) / (sum_j' s_e(j') + 1e-20),
+ *           times routed_scale: of the scores, without the bias
+ * Equal values go to the lower index, everywhere. Then n_shared slots with ids
+ * E, E+1, ... and weight 1, as in moe_route(): rows of topk_ids and topk_w hold
+ * k + n_shared entries.
+ *   logits  [B][E] logits_dtype (moed_dtype);  bias [E] float32 or NULL
+ * The scores are computed in 64 bits, so that they, and what is chosen by them,
+ * are the same wherever this definition is followed. Experts whose logit or
+ * bias is NaN, or whose bias is -infinity, are never chosen and add nothing to
+ * their group; a group without any other is never chosen (one with a single one
+ * is worth that one's choice). In a softmax a NaN logit adds nothing, and
+ * exp(l - m) is 1 where l equals an infinite m. Where fewer than k experts can
+ * be chosen the missing slots get id -1 (the layer then writes NaN for that
+ * token) and a NaN weight, and the sum is of the others.
+ * Limits (MOED_ERR_SHAPE): E <= 2048, 1 <= n_group <= 64, a divisor of E;
+ * 1 <= topk_group <= n_group; 1 <= k <= 64 and at most topk_group * E / n_group;
+ * n_shared >= 0; B*E and B*(k + n_shared) below 2^31. Unknown logits_dtype,
+ * score or group_score: MOED_ERR_DTYPE. B = 0 launches nothing.
+ */
+int moe_route_scored(const void *logits, int logits_dtype, const float *bias, int score,
+                     int n_group, int topk_group, int group_score, int renormalize,
+                     int B, int E, int k, int n_shared, float routed_scale,
+                     int32_t *topk_ids, float *topk_w, void *stream);
+
+typedef enum {
+    MOED_GATE_NONE = 0,
+    MOED_GATE_TOKEN = 1,     /* gate [B]                                         */
+    MOED_GATE_CHANNEL = 2,   /* gate [H]                                         */
+    MOED_GATE_FULL = 3       /* gate [B][H]                                      */
+} moed_gate;
+
+/*
+ * The end of a block and the norm in front of the next one:
+ *   y          the block's output [B][H], or, with a position, the weighted sum
+ *              of the experts' rows that moe_combine() takes:
+ *              sum_j topk_w[b][j] * y[position[b][j]]
+ *   t          = y / sqrt(mean_h y^2 + post_eps) * post_gain   (y without post_gain)
+ *   s          = residual_scale * residual + scale * act(gate) * t
+ *   residual_out = s rounded to the residual's type
+ *   out        = s / sqrt(mean_h s^2 + eps) * gain             (of the unrounded s)
+ *   out_q, out_s  the same in MXFP8, by the rule of moe_norm()
+ * all in float32, without a rounding in between.
+ *   y          [B][H] y_dtype; [R][H] with a position
+ *   position   [B][k] int32 (a place outside [0, R) makes the token's outputs
+ *              NaN) with topk_w [B][k] float32; both NULL: y is [B][H] (R and k
+ *              are not used)
+ *   post_gain  [H] post_gain_dtype, or NULL
+ *   gate       a moed_gate shape of gate_dtype; NULL with MOED_GATE_NONE
+ *   gate_act   MOED_ACT_NONE, MOED_ACT_SIGMOID or MOED_ACT_TANH
+ *   residual   [B][H] residual_dtype
+ *   residual_out  [B][H] residual_dtype, or NULL: not stored; may be the residual,
+ *              or y [B][H] where the types agree
+ *   gain       [H] gain_dtype, or NULL where nothing is normed (then out, out_q
+ *              and out_s are NULL)
+ *   out        [B][H] out_dtype, or NULL; may be y [B][H] or the residual where the
+ *              types agree
+ *   out_q, out_s  [B][H] codes and [B][H/32] scales, or both NULL
+ * One of residual_out, out and out_q must be given. Outputs overlap nothing
+ * else; out and residual_out are not the same (MOED_ERR_SHAPE). Squares as in
+ * moe_norm().
+ * Limits (MOED_ERR_SHAPE): 1 <= H <= 32768, a multiple of 32 with out_q;
+ * eps, post_eps >= 0; with a position 1 <= k <= 64 and 0 <= R < 2^28. Pointers of
+ * y, post_gain, residual, residual_out, gain, out and out_q are 16-byte aligned,
+ * and the gate's (MOED_ERR_ALIGN). B = 0 launches nothing.
+ */
+int moe_post_norm(const void *y, int y_dtype, int R, const int32_t *position, const float *topk_w, int k,
+                  const void *post_gain, int post_gain_dtype, float post_eps,
+                  const void *gate, int gate_dtype, int gate_shape, int gate_act, float scale,
+                  const void *residual, int residual_dtype, float residual_scale, void *residual_out,
+                  const void *gain, int gain_dtype, float eps, void *out, int out_dtype,
+                  uint8_t *out_q, uint8_t *out_s, int B, int H, void *stream);
+
 /* Human-readable name of a moed_status value. Never NULL. */
 const char *moed_status_string(int status);
 

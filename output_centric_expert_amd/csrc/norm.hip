@@ -24,80 +24,11 @@
 // largest value is found with two DPP steps.
 #include "mx_encode.h"
 #include "prompt.h"
+#include "row_values.h"
 
 namespace moed {
 
 namespace {
-
-__device__ __forceinline__ float bf16_val(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-
-// V consecutive values of a bf16 or float32 array as float32.
-template <bool BF16, bool NT, int V>
-__device__ __forceinline__ void load_vals(const void* p, size_t at, float (&v)[V])
-{
-    if constexpr (V == 1) {
-        v[0] = BF16 ? bf16_val(static_cast<const uint16_t*>(p)[at]) : static_cast<const float*>(p)[at];
-    } else if constexpr (BF16) {
-        const u32x4 u = ld<NT>(reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + at));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = bf16_lo(u[i]);
-            v[2 * i + 1] = bf16_hi(u[i]);
-        }
-    } else {
-        const f32x4 a = ld<NT>(reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + at));
-        const f32x4 b = ld<NT>(reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + at + 4));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = a[i];
-            v[4 + i] = b[i];
-        }
-    }
-}
-
-template <bool BF16, int V>
-__device__ __forceinline__ void store_vals(void* p, size_t at, const float (&v)[V])
-{
-    if constexpr (V == 1) {
-        if constexpr (BF16)
-            static_cast<uint16_t*>(p)[at] = f32_to_bf16_rne(v[0]);
-        else
-            static_cast<float*>(p)[at] = v[0];
-    } else if constexpr (BF16) {
-        u32x4 u;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            u[i] = f32x2_to_bf16x2_rne(v[2 * i], v[2 * i + 1]);
-        __builtin_nontemporal_store(u, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + at));
-    } else {
-        __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4*>(static_cast<float*>(p) + at));
-        __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, reinterpret_cast<f32x4*>(static_cast<float*>(p) + at + 4));
-    }
-}
-
-// Squares of a row whose sum is below 2^-80 (all |s| < 2^-40) may underflow, and its reciprocal root may pass
-// float32's range. With an eps as small (TINY) the row is then taken times 2^100, and eps times 2^200, which changes
-// nothing else: values from the smallest subnormal number to 2^60, their squares from 2^-98 to 2^120. Above, what is
-// lost to underflow is at most 2^15 squares below 2^-126 each: 2^-31 of the sum, or of eps. A kernel of its own, because
-// the test costs the others: a token of 2048 2.19 instead of 2.10 us, 8192 tokens of 2049 112.7 instead of 110.1.
-constexpr float kSmall = 0x1p-80f, kLift = 0x1p100f;
-
-// Sum over the threads of a row (one wavefront, or all of the workgroup), in every one of them.
-template <int W>
-__device__ __forceinline__ float row_sum(float v, float* part)
-{
-    v = wave_sum(v);
-    if constexpr (W > 1) {
-        if (threadIdx.x % kWave == 0)
-            part[threadIdx.x / kWave] = v;
-        __syncthreads();
-        v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < W; ++w)
-            v += part[w];
-    }
-    return v;
-}
 
 // RES: 0 no residual, 1 bfloat16, 2 float32. TINY: eps < kSmall.
 template <int V, int NV, int TPR, bool XBF16, int RES, bool TINY>

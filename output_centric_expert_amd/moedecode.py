@@ -28,7 +28,8 @@ EXPORTS = ("moed_workspace_bytes", "moe_decode", "moe_decode_gate_up", "moe_deco
            "moed_last_hip_error", "moed_tuning_init", "moe_decode_tuned", "moe_decode_gate_up_tuned",
            "moe_decode_down_tuned", "moe_decode_noalloc", "moed_bench_read_cfg", "moe_norm",
            "moe_group_workspace_bytes", "moe_group", "moe_grouped_workspace_bytes", "moe_grouped_gate_up",
-           "moe_grouped_matmul", "moe_combine", "moe_prefill_workspace_bytes", "moe_prefill")
+           "moe_grouped_matmul", "moe_combine", "moe_prefill_workspace_bytes", "moe_prefill",
+           "moe_linear_workspace_bytes", "moe_linear", "moe_route_scored", "moe_post_norm")
 
 
 class MoedTuning(ctypes.Structure):
@@ -97,6 +98,15 @@ def load() -> ctypes.CDLL:
         lib.moe_prefill_workspace_bytes.restype = Z
         lib.moe_prefill.argtypes = [P, P, I] + [P] * 8 + [I, P, I] + [I] * 5 + [P, Z, P]
         lib.moe_prefill.restype = I
+        F = ctypes.c_float
+        lib.moe_linear_workspace_bytes.argtypes = [I] * 5
+        lib.moe_linear_workspace_bytes.restype = Z
+        lib.moe_linear.argtypes = [P, I, P, I, P, I, I, P, I, P, I, I, I, I, P, Z, P]
+        lib.moe_linear.restype = I
+        lib.moe_route_scored.argtypes = [P, I, P] + [I] * 9 + [F, P, P, P]
+        lib.moe_route_scored.restype = I
+        lib.moe_post_norm.argtypes = [P, I, I, P, P, I, P, I, F, P, I, I, I, F, P, I, F, P, P, I, F, P, I, P, P, I, I, P]
+        lib.moe_post_norm.restype = I
         lib.moed_selftest_decode.argtypes = [P, P, P, I, I, P]
         lib.moed_selftest_decode.restype = I
         lib.moed_bench_read.argtypes = [P, Z, P, Z, P]
@@ -565,6 +575,149 @@ def moe_prefill(x, topk_ids, topk_w, wg_q, wg_s, wu_q, wu_s, wd_q, wd_s, x_s=Non
         _arg(workspace, "workspace", _U8, None, dev), workspace.numel(), _raw_stream(stream, dev))
     _check(st, "moe_prefill")
     return out
+
+
+# ---------------------------------------------------------------- around the block
+
+_ACT = {None: 0, "silu": 1, "gelu": 2, "gelu_tanh": 3, "relu": 4, "sigmoid": 5, "tanh": 6}      # moed_activation
+_SCORE = {"softmax": 0, "sigmoid": 1}            # moed_score
+_GATE_ACT = {None: 0, "sigmoid": 5, "tanh": 6}
+_GROUP = {"max": 0, "top2": 1}                   # moed_group_score
+
+
+def _choice(table, value, name):
+    try:
+        return table[value]
+    except (KeyError, TypeError):
+        raise ValueError(f"{name}: {value!r} is none of {', '.join(map(repr, table))}") from None
+
+
+def moe_linear_workspace_bytes(B: int, K: int, N: int, x_dtype=torch.bfloat16, w_dtype=torch.bfloat16) -> int:
+    """Workspace of moe_linear (0: none is needed)."""
+    return int(load().moe_linear_workspace_bytes(B, K, N, _DT[x_dtype], _DT[w_dtype]))
+
+
+def moe_linear(x, w, bias=None, activation=None, residual=None, out=None, out_dtype=torch.bfloat16, workspace=None,
+               stream=None):
+    """Dense product with an epilogue: returns out [B, N] = act(x @ w.T + bias) + residual, rounded once.
+
+    x [B, K], w [N, K], bias [N] and residual [B, N] are bfloat16 or float32 each. activation: None, "silu", "gelu",
+    "gelu_tanh", "relu", "sigmoid" or "tanh". residual may be out, for an update in place."""
+    dev = torch.cuda.current_device()
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("expected x [B, K] and w [N, K]")
+    B, K = x.shape
+    N = w.shape[0]
+    act = _choice(_ACT, activation, "activation")
+    xp, wp = _arg(x, "x", _F, None, dev), _arg(w, "w", _F, (N, K), dev)
+    bp, rp = _opt(bias, "bias", _F, (N,), dev), _opt(residual, "residual", _F, (B, N), dev)
+    out, op = _result(out, "out", _F, (B, N), dev, out_dtype, x, stream)
+    lib = load()
+    xd, wd = _DT[x.dtype], _DT[w.dtype]
+    sp = sb = 0
+    if workspace is not None:
+        sp, sb = _arg(workspace, "workspace", _U8, None, dev), workspace.numel()
+    else:
+        need = lib.moe_linear_workspace_bytes(B, K, N, xd, wd)
+        if need:
+            workspace = _new((need,), torch.uint8, x, stream)
+            sp, sb = workspace.data_ptr(), need
+    st = lib.moe_linear(xp, xd, wp, wd, bp, _DT[bias.dtype] if bias is not None else 0, act, rp,
+                        _DT[residual.dtype] if residual is not None else 0, op, _DT[out.dtype], B, K, N, sp, sb,
+                        _raw_stream(stream, dev))
+    _check(st, "moe_linear")
+    return out
+
+
+def moe_route_scored(logits, k: int, score: str = "sigmoid", bias=None, n_group: int = 1, topk_group: int = 1,
+                     group_score: str = "top2", renormalize: bool = True, n_shared: int = 0, routed_scale: float = 1.0,
+                     ids=None, w=None, stream=None):
+    """Router by scores, a bias for balance and groups of experts: (topk_ids int32, topk_w float32), both
+    [B, k+n_shared], from logits [B, E] (bfloat16 or float32).
+
+    The k experts of the largest score + bias ("sigmoid" or "softmax" scores, bias float32 [E] or None) among the
+    topk_group of n_group groups whose largest ("max"), or two largest ("top2"), of these are worth most; their
+    weights are the scores without the bias, divided by their sum with renormalize, times routed_scale. Shared slots
+    get ids E, E+1, ... and weight 1."""
+    dev = torch.cuda.current_device()
+    if logits.dim() != 2:
+        raise ValueError("logits: expected shape [B, E]")
+    B, E = logits.shape
+    kt = k + n_shared
+    lp, bp = _arg(logits, "logits", _F, None, dev), _opt(bias, "bias", _F32, (E,), dev)
+    sc, gs = _choice(_SCORE, score, "score"), _choice(_GROUP, group_score, "group_score")
+    if min(k, n_shared) < 0:
+        raise ValueError("k and n_shared are not negative")
+    ids, ip = _result(ids, "ids", _I32, (B, kt), dev, torch.int32, logits, stream)
+    w, wp = _result(w, "w", _F32, (B, kt), dev, torch.float32, logits, stream)
+    st = load().moe_route_scored(lp, _DT[logits.dtype], bp, sc, n_group, topk_group, gs, renormalize, B, E, k, n_shared,
+                                 routed_scale, ip, wp, _raw_stream(stream, dev))
+    _check(st, "moe_route_scored")
+    return ids, w
+
+
+def moe_post_norm(y, residual, post_gain=None, post_eps: float = 1e-6, gate=None, gate_act=None, scale: float = 1.0,
+                  residual_scale: float = 1.0, gain=None, eps: float = 1e-6, position=None, topk_w=None,
+                  out_dtype=torch.bfloat16, quantize: bool = False, out=None, residual_out=None, out_q=None, out_s=None,
+                  stream=None):
+    """The end of a block and the norm in front of the next: returns (out, residual_out, out_q, out_s).
+
+    residual_out = residual_scale * residual + scale * act(gate) * t in the residual's type, with t = RMSNorm(y) *
+    post_gain (y itself without post_gain); out = RMSNorm(residual_out, unrounded) * gain in out_dtype (None: no plain
+    output; without gain there is no norm and no output); with quantize, out_q uint8 [B, H] and out_s uint8 [B, H/32]
+    are out's values in MXFP8, else None.
+    y is [B, H]; with position int32 [B, k] and topk_w float32 [B, k] it is the experts' rows [R, H], and their weighted
+    sum (moe_combine's) is taken. gate: one number a token [B, 1], a channel [H] or [1, H], or each [B, H]; gate_act:
+    None, "sigmoid" or "tanh". Give the residual as residual_out for an update in place."""
+    dev = torch.cuda.current_device()
+    if y.dim() != 2 or residual.dim() != 2:
+        raise ValueError("expected y [B, H] (or [R, H] with position) and residual [B, H]")
+    B, H = residual.shape
+    rp, rd = _arg(residual, "residual", _F, None, dev), residual.dtype
+    pp = tp = gp = None
+    R = k = shape = 0
+    if position is not None:
+        if topk_w is None or position.dim() != 2:
+            raise ValueError("position: expected shape [B, k], with topk_w")
+        R, k = y.shape[0], position.shape[1]
+        yp = _arg(y, "y", _F, (R, H), dev)
+        pp, tp = _arg(position, "position", _I32, (B, k), dev), _arg(topk_w, "topk_w", _F32, (B, k), dev)
+    elif topk_w is not None:
+        raise ValueError("topk_w needs position")
+    else:
+        yp = _arg(y, "y", _F, (B, H), dev)
+    if gate is not None:
+        gs = tuple(gate.shape) if isinstance(gate, torch.Tensor) else None
+        shape = 3 if gs == (B, H) else 2 if gs in ((H,), (1, H)) else 1
+        gp = _arg(gate, "gate", _F, gs if shape > 1 else (B, 1), dev)
+    elif gate_act is not None:
+        raise ValueError("gate_act needs a gate")
+    act = _choice(_GATE_ACT, gate_act, "gate_act")
+    if quantize and H % 32:
+        raise ValueError("quantize needs H to be a multiple of 32")
+    residual_out, rop = _result(residual_out, "residual_out", (rd,), (B, H), dev, rd, residual, stream)
+    op = qp = sp = None
+    if gain is None:
+        if out is not None or quantize or out_q is not None or out_s is not None:
+            raise ValueError("out, quantize, out_q and out_s need a gain")
+    else:
+        if out is not None or out_dtype is not None:
+            out, op = _result(out, "out", _F, (B, H), dev, out_dtype, residual, stream)
+        if quantize:
+            out_q, qp = _result(out_q, "out_q", _U8, (B, H), dev, torch.uint8, residual, stream)
+            out_s, sp = _result(out_s, "out_s", _U8, (B, H // 32), dev, torch.uint8, residual, stream)
+        elif out_q is not None or out_s is not None:
+            raise ValueError("out_q and out_s need quantize=True")
+        elif out is None:
+            raise ValueError("gain needs an output: out_dtype or quantize")
+    st = load().moe_post_norm(
+        yp, _DT[y.dtype], R, pp, tp, k, _opt(post_gain, "post_gain", _F, (H,), dev),
+        _DT[post_gain.dtype] if post_gain is not None else 0, post_eps, gp, _DT[gate.dtype] if gate is not None else 0,
+        shape, act, scale, rp, _DT[rd], residual_scale, rop, _opt(gain, "gain", _F, (H,), dev),
+        _DT[gain.dtype] if gain is not None else 0, eps, op, _DT[out.dtype] if out is not None else 0, qp, sp, B, H,
+        _raw_stream(stream, dev))
+    _check(st, "moe_post_norm")
+    return out, residual_out, out_q, out_s
 
 
 def moed_selftest_decode(codes, scales, path: int, out=None, stream=None):
