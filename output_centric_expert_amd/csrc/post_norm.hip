@@ -10,7 +10,7 @@
 // of the first sum, so that a row waits for memory once. Memory bound.
 // Rows whose length is no multiple of 8 begin at any element; their pieces are loaded as they lie, and the last one
 // value by value.
-#include "block.h"
+#include "activation.h"
 #include "mx_encode.h"
 #include "row_values.h"
 
@@ -50,11 +50,7 @@ __device__ __forceinline__ void load_piece(bool bf16, const void* p, size_t at, 
 
 __device__ __forceinline__ float gate_value(float g, int act)
 {
-    if (act == kActSigmoid)
-        return 1.0f / (1.0f + expf(-g));
-    if (act == kActTanh)
-        return tanhf(g);
-    return g;
+    return act == kActSigmoid ? sigmoid(g) : act == kActTanh ? tanh_of(g) : g;
 }
 
 // 1 / sqrt(mean of squares + eps) of a row as mul * scale: mul is 1 but for rows whose squares would underflow

@@ -19,6 +19,7 @@
 
 #include <type_traits>
 
+#include "lds_loads.h"
 #include "product_common.h"
 
 namespace moed {
@@ -37,23 +38,6 @@ __device__ __forceinline__ bool exact_scale(uint32_t c)
 }
 
 static __device__ const u32x4 kZeros = {0, 0, 0, 0};   // source of the values behind the end of a row
-
-// 16 bytes per lane from global memory straight to LDS: lane i of the wavefront
-// writes base + 16 i (base uniform). No register receives the data; the caller
-// waits on vmcnt before a barrier. Written as asm because the compiler makes
-// every later LDS read wait for the builtin's load, whatever buffer it fills.
-// The address is a uniform base plus a lane's 32-bit offset.
-__device__ __forceinline__ void load_to_lds16(const uint8_t* from, uint32_t offset, uint32_t base)
-{
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(from), "s"(base)
-                 : "memory", "m0");
-}
-
-// The same from an address of each lane's own.
-__device__ __forceinline__ void load_to_lds16(const uint8_t* from, uint32_t base)
-{
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(base) : "memory", "m0");
-}
 
 __device__ __forceinline__ void load_to_lds4(const void* from, uint32_t base)
 {
@@ -95,12 +79,6 @@ struct Shape {
     static constexpr int kWeightLoads = kBN * kWU / kThreads;
 };
 
-template <int N>
-__device__ __forceinline__ void wait_loads()
-{
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-
 // Units of a row are stored at c ^ swizzle(row), so that the lanes that read one
 // unit of 8 neighbouring rows together meet different banks.
 template <int UNITS>
@@ -116,8 +94,6 @@ __device__ __forceinline__ int unit_at(int col, int c)
 {
     return (col * UNITS + (c ^ swizzle<UNITS>(col))) * 16;
 }
-
-__device__ __forceinline__ u32x4 lds16(const uint8_t* p) { return *reinterpret_cast<const u32x4*>(p); }
 
 // f(N) with the smallest of RT, RT/2, RT/4 .. (as a constant) that is at least
 // `live`: a tile's last rows take no more matrix instructions than they need.

@@ -69,7 +69,7 @@ def check_linear(x, w, bias, act, residual, out):
 SIZES = [(1, 1, 1), (1, 2048, 128), (1, 7168, 256), (2, 33, 5), (3, 1111, 777), (4, 8, 4096), (5, 4096, 1), (7, 100, 300),
          (8, 2048, 512), (9, 512, 16), (16, 7168, 256), (17, 63, 65), (31, 2049, 130), (32, 4096, 1024), (33, 64, 33),
          (64, 7168, 256), (65, 200, 257), (127, 1000, 96), (128, 128, 128), (200, 20000, 40), (256, 256, 512), (300, 1, 300),
-         (1000, 1111, 777), (513, 4104, 520), (2048, 96, 8), (2500, 7, 3), (1024, 1024, 1024), (4096, 520, 264)]
+         (1000, 1111, 777), (513, 4104, 520), (2048, 96, 8), (2500, 7, 3), (1024, 1024, 1024), (4096, 520, 264), (4100, 264, 4100), (4100, 77, 4099)]
 
 
 @pytest.mark.parametrize("B,K,N", SIZES)
