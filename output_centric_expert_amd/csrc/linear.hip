@@ -77,81 +77,118 @@ moe_linear_dot_kernel(LinearArgs p, int n_blocks)
         linear_store(p, v, b, n);
 }
 
-// The sums of a product whose k was split, added in the order of the splits, and the epilogue.
+// The sums of a product whose k was split, added in the order of the splits, and the epilogue. V neighbouring outputs of a
+// row a thread (fewer at its end).
+template <int V>
 __global__ void __launch_bounds__(256)
-moe_linear_join_kernel(LinearArgs p, const float* partial, int splits)
+moe_linear_join_kernel(LinearArgs p, const float* partial, int splits, unsigned threads)
 {
-    const size_t count = (size_t)p.B * (size_t)p.N;
-    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= count)
+    const unsigned i = blockIdx.x * 256u + threadIdx.x;
+    if (i >= threads)
         return;
-    float v = 0.0f;
+    const unsigned pieces = ((unsigned)p.N + V - 1) / V, b = i / pieces;
+    const int n = (int)(i - b * pieces) * V, have = p.N - n;
+    const size_t at = (size_t)b * (size_t)p.N + (size_t)n, count = (size_t)p.B * (size_t)p.N;
+    if constexpr (V == 1) {
+        float v = 0.0f;
 #pragma unroll 4
-    for (int q = 0; q < splits; ++q)
-        v += partial[q * count + i];
-    const size_t b = i / (unsigned)p.N;
-    linear_store(p, v, b, (int)(i - b * (unsigned)p.N));
+        for (int q = 0; q < splits; ++q)
+            v += partial[q * count + at];
+        linear_store(p, v, b, n);
+    } else {
+        float v[8] = {}, bias[8] = {}, residual[8] = {};
+#pragma unroll 2
+        for (int q = 0; q < splits; ++q) {
+            float o[8];
+            load_any<false, true>(partial, q * count + at, have, o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] += o[e];
+        }
+        if (p.bias)
+            load_some(p.bias_bf16, p.bias, (size_t)n, have, bias);
+        if (p.residual)
+            load_some(p.residual_bf16, p.residual, at, have, residual);
+        linear_finish(p, bias, residual, v);
+        store_some(p.out_bf16, p.out, at, have, v);
+    }
 }
 
 namespace {
 
 constexpr int kDotRows = 1;                       // up to here the rows are multiplied without matrix instructions
-constexpr int kSkinnyRows = 64;                   // rows of the smaller side up to which it is a skinny product
+constexpr int kSkinnyTiles = 400;                 // tiles up to which a product of more than 16 rows is a skinny one
 
-TileSize tile_of(bool x_bf16, bool w_bf16, int tile)
-{
-    return x_bf16 ? (w_bf16 ? linear_tile_bf16(tile) : linear_tile_mixed_w(tile))
-                  : (w_bf16 ? linear_tile_mixed_x(tile) : linear_tile_f32(tile));
-}
-
-enum class Kind { dot, skinny, tiled };
 struct Choice {
-    Kind kind;
-    int tile, rt;
+    enum Kind { dot, skinny, tiled } kind;
+    int tile, rt, splits;
     bool swapped;
     LinearPlan plan;
-    SkinnyPlan skinny;
+    SkinnyPlan skinny_plan;
 };
 
+bool tile_cost(bool x_bf16, bool w_bf16, int tile, TileCost* t)
+{
+    return x_bf16 ? (w_bf16 ? linear_cost_bf16(tile, t) : linear_cost_mixed_w(tile, t))
+                  : (w_bf16 ? linear_cost_mixed_x(tile, t) : linear_cost_f32(tile, t));
+}
+
+// The kernel by the sizes.
 Choice choose(int B, int K, int N, bool x_bf16, bool w_bf16)
 {
     Choice c;
+    c.tile = c.rt = 0;
+    c.splits = 1;
+    c.swapped = false;
     if (B <= kDotRows) {
-        c.kind = Kind::dot;
+        c.kind = Choice::dot;
         return c;
     }
-    if (B <= kSkinnyRows || N <= kSkinnyRows) {
-        c.kind = Kind::skinny;
+    const int step = !x_bf16 && !w_bf16 ? 32 : 64;
+    {
         c.swapped = N < B;
         const int few = c.swapped ? N : B, many = c.swapped ? B : N;
         c.rt = few <= 16 ? 1 : 2;
-        c.skinny.few_blocks = (few + 16 * c.rt - 1) / (16 * c.rt);
-        c.skinny.many_blocks = (many + 15) / 16;
-        const int steps = (K + (!x_bf16 && !w_bf16 ? 31 : 63)) / (!x_bf16 && !w_bf16 ? 32 : 64);
-        const long long tiles = (long long)c.skinny.few_blocks * c.skinny.many_blocks;
-        long long splits = 256 / tiles, most = steps / (2 * kSkinnyWaves);
-        splits = splits < most ? splits : most;
-        c.skinny.splits = (int)(splits < 1 ? 1 : splits > 16 ? 16 : splits);
-        return c;
+        SkinnyPlan& s = c.skinny_plan;
+        s.few_blocks = (few + 16 * c.rt - 1) / (16 * c.rt);
+        s.many_blocks = (many + 15) / 16;
+        const long long tiles = (long long)s.few_blocks * s.many_blocks;
+        if (few <= 16 || tiles <= kSkinnyTiles) {
+            c.kind = Choice::skinny;
+            // workgroups for the whole chip, but a step and a half at least for a wavefront
+            long long splits = 256 / tiles;
+            const long long most = (K + step - 1) / step * 2 / (3 * kSkinnyWaves);
+            splits = splits < most ? splits : most;
+            c.splits = s.splits = (int)(splits < 1 ? 1 : splits);
+            return c;
+        }
     }
-    c.kind = Kind::tiled;
-    c.tile = kTileMiddle;
-    TileSize t = tile_of(x_bf16, w_bf16, kTileLarge);
-    const long long large = ((B + t.rows - 1LL) / t.rows) * ((N + t.outputs - 1LL) / t.outputs);
-    if (large >= 256)
-        c.tile = kTileLarge;
-    t = tile_of(x_bf16, w_bf16, c.tile);
-    c.plan.m_blocks = (B + t.rows - 1) / t.rows;
-    c.plan.n_blocks = (N + t.outputs - 1) / t.outputs;
+    c.kind = Choice::tiled;
+    // Of the tiles and ways to split k the one that should take least: some us to begin and end, a step's time for each
+    // round of the chip's workgroups, and for split k a second launch and its bytes.
+    const float outputs = (float)B * (float)N;
+    float best = 0.0f;
+    TileCost t;
+    for (int i = 0; tile_cost(x_bf16, w_bf16, i, &t); ++i) {
+        const int m_blocks = (B + t.rows - 1) / t.rows, n_blocks = (N + t.outputs - 1) / t.outputs, steps = (K + t.k - 1) / t.k;
+        const long long tiles = (long long)m_blocks * n_blocks;
+        for (int splits = 1; splits <= 16 && (splits == 1 || (tiles * splits <= 512 && steps >= 7 * splits)); ++splits) {
+            const int each = (steps + splits - 1) / splits;
+            const long long groups = tiles * splits;
+            const float rounds = t.paired > 0.0f && groups > 256 ? (float)((groups + 511) / 512) * t.paired
+                                                                  : (float)((groups + 255) / 256) * t.alone;
+            const float us = 4.0f + (float)each * rounds + (splits > 1 ? 3.0f + outputs * (float)splits * 1.6e-6f : 0.0f);
+            if ((i == 0 && splits == 1) || us < best) {
+                best = us;
+                c.tile = i;
+                c.plan.m_blocks = m_blocks;
+                c.plan.n_blocks = n_blocks;
+                c.plan.split_steps = each;
+                c.splits = c.plan.splits = (steps + each - 1) / each;
+            }
+        }
+    }
     c.plan.group = c.plan.n_blocks < 8 ? c.plan.n_blocks : 8;
-    const int steps = (K + t.k - 1) / t.k;
-    const long long tiles = (long long)c.plan.m_blocks * c.plan.n_blocks;
-    long long splits = tiles >= 256 ? 1 : 512 / tiles;
-    splits = splits < steps / 4 ? splits : steps / 4;
-    splits = splits < 1 ? 1 : splits > 32 ? 32 : splits;
-    c.plan.split_steps = (int)((steps + splits - 1) / splits);
-    c.plan.splits = (steps + c.plan.split_steps - 1) / c.plan.split_steps;
-    c.plan.partial = nullptr;
     return c;
 }
 
@@ -160,8 +197,7 @@ Choice choose(int B, int K, int N, bool x_bf16, bool w_bf16)
 size_t linear_workspace(int B, int K, int N, bool x_bf16, bool w_bf16)
 {
     const Choice c = choose(B, K, N, x_bf16, w_bf16);
-    const int splits = c.kind == Kind::tiled ? c.plan.splits : c.kind == Kind::skinny ? c.skinny.splits : 1;
-    return splits > 1 ? (size_t)splits * (size_t)B * (size_t)N * 4 : 0;
+    return c.splits > 1 ? (size_t)c.splits * (size_t)B * (size_t)N * 4 : 0;
 }
 
 namespace {
@@ -172,6 +208,19 @@ hipError_t launch_dot_shape(const LinearArgs& p, hipStream_t s)
     const int per = NW * (kDotWaves / KS), nb = (p.N + per - 1) / per;
     const unsigned grid = (unsigned)((long long)nb * ((p.B + RB - 1) / RB));
     hipLaunchKernelGGL((moe_linear_dot_kernel<X, W, RB, NW, KS>), dim3(grid), dim3(kDotWaves * kWave), 0, s, p, nb);
+    return hipGetLastError();
+}
+
+hipError_t launch_join(const LinearArgs& p, const float* partial, int splits, hipStream_t s)
+{
+    // below, single outputs fill the chip sooner
+    if ((size_t)p.B * (size_t)p.N >= 1u << 18) {
+        const unsigned threads = (unsigned)p.B * (((unsigned)p.N + 7) / 8);
+        hipLaunchKernelGGL(moe_linear_join_kernel<8>, dim3((threads + 255) / 256), dim3(256), 0, s, p, partial, splits, threads);
+    } else {
+        const unsigned threads = (unsigned)p.B * (unsigned)p.N;
+        hipLaunchKernelGGL(moe_linear_join_kernel<1>, dim3((threads + 255) / 256), dim3(256), 0, s, p, partial, splits, threads);
+    }
     return hipGetLastError();
 }
 
@@ -186,29 +235,23 @@ hipError_t launch_dot(const LinearArgs& p, hipStream_t s)
 hipError_t launch_linear(const LinearArgs& p, bool x_bf16, bool w_bf16, void* workspace, hipStream_t s)
 {
     Choice c = choose(p.B, p.K, p.N, x_bf16, w_bf16);
-    if (c.kind == Kind::dot) {
+    if (c.kind == Choice::dot) {
         if (x_bf16)
             return w_bf16 ? launch_dot<true, true>(p, s) : launch_dot<true, false>(p, s);
         return w_bf16 ? launch_dot<false, true>(p, s) : launch_dot<false, false>(p, s);
     }
-    c.plan.partial = c.skinny.partial = static_cast<float*>(workspace);
+    c.plan.partial = c.skinny_plan.partial = static_cast<float*>(workspace);
     hipError_t e;
-    int splits;
-    if (c.kind == Kind::skinny) {
+    if (c.kind == Choice::skinny) {
         auto launch = x_bf16 ? (w_bf16 ? launch_skinny_bf16 : launch_skinny_mixed_w) : (w_bf16 ? launch_skinny_mixed_x : launch_skinny_f32);
-        e = launch(c.swapped, c.rt, p, c.skinny, s);
-        splits = c.skinny.splits;
+        e = launch(c.swapped, c.rt, p, c.skinny_plan, s);
     } else {
         auto launch = x_bf16 ? (w_bf16 ? launch_linear_bf16 : launch_linear_mixed_w) : (w_bf16 ? launch_linear_mixed_x : launch_linear_f32);
         e = launch(c.tile, p, c.plan, s);
-        splits = c.plan.splits;
     }
-    if (e != hipSuccess || splits == 1)
+    if (e != hipSuccess || c.splits == 1)
         return e;
-    const size_t count = (size_t)p.B * (size_t)p.N;
-    hipLaunchKernelGGL(moe_linear_join_kernel, dim3((unsigned)((count + 255) / 256)), dim3(256), 0, s, p,
-                       static_cast<const float*>(workspace), splits);
-    return hipGetLastError();
+    return launch_join(p, static_cast<const float*>(workspace), c.splits, s);
 }
 
 }  // namespace moed

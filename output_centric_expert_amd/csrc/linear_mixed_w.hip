@@ -4,11 +4,29 @@
 
 namespace moed {
 
-TileSize linear_tile_mixed_w(int tile) { return tile_size<false, true>(tile); }
+namespace {
+
+constexpr TileCost kTiles[] = {
+    {256, 128, 64, 2.45f, 0.00f},
+    {64, 64, 64, 0.80f, 1.05f}};
+
+}  // namespace
+
+bool linear_cost_mixed_w(int tile, TileCost* cost)
+{
+    if (tile >= (int)(sizeof kTiles / sizeof kTiles[0]))
+        return false;
+    *cost = kTiles[tile];
+    return true;
+}
 
 hipError_t launch_linear_mixed_w(int tile, const LinearArgs& p, const LinearPlan& plan, hipStream_t s)
 {
-    return launch_tile<false, true>(tile, p, plan, s);
+    switch (tile) {
+    case 0: return launch_linear_tile<false, true, 8, 2, 2, 4, 2>(p, plan, s);
+    case 1: return launch_linear_tile<false, true, 2, 1, 2, 4, 2>(p, plan, s);
+    default: return hipErrorInvalidValue;
+    }
 }
 
 hipError_t launch_skinny_mixed_w(bool swapped, int rt, const LinearArgs& p, const SkinnyPlan& plan, hipStream_t s)

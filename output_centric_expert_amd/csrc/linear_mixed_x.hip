@@ -4,11 +4,29 @@
 
 namespace moed {
 
-TileSize linear_tile_mixed_x(int tile) { return tile_size<true, false>(tile); }
+namespace {
+
+constexpr TileCost kTiles[] = {
+    {128, 256, 64, 2.60f, 0.00f},
+    {64, 128, 64, 0.95f, 1.50f}};
+
+}  // namespace
+
+bool linear_cost_mixed_x(int tile, TileCost* cost)
+{
+    if (tile >= (int)(sizeof kTiles / sizeof kTiles[0]))
+        return false;
+    *cost = kTiles[tile];
+    return true;
+}
 
 hipError_t launch_linear_mixed_x(int tile, const LinearArgs& p, const LinearPlan& plan, hipStream_t s)
 {
-    return launch_tile<true, false>(tile, p, plan, s);
+    switch (tile) {
+    case 0: return launch_linear_tile<true, false, 4, 4, 2, 4, 2>(p, plan, s);
+    case 1: return launch_linear_tile<true, false, 1, 4, 4, 2, 2>(p, plan, s);
+    default: return hipErrorInvalidValue;
+    }
 }
 
 hipError_t launch_skinny_mixed_x(bool swapped, int rt, const LinearArgs& p, const SkinnyPlan& plan, hipStream_t s)

@@ -38,7 +38,8 @@ struct SkinnyShape {
 
 }  // namespace
 
-// SWAPPED: the side with few rows is w, that with many x. DIRECT: rows begin at 16-byte borders.
+// SWAPPED: the side with few rows is w, that with many x. DIRECT: rows begin at dwords (no bfloat16 rows of odd K), so that
+// whole steps go straight to LDS.
 template <bool FEW32, bool MANY32, bool SWAPPED, bool DIRECT, int RT>
 __global__ void __launch_bounds__(kSkinnyWaves * kWave)
 moe_linear_skinny_kernel(LinearArgs p, SkinnyPlan plan)
@@ -70,15 +71,34 @@ moe_linear_skinny_kernel(LinearArgs p, SkinnyPlan plan)
     for (int i = 0; i < S::kFewLoads; ++i) {
         const int r = i * (kWave / S::kFU) + lane / S::kFU;
         foff[i] = (uint32_t)(few0 + (r < flast ? r : flast)) * (uint32_t)((size_t)p.K * (FEW32 ? 4 : 2));
-        funit[i] = (lane % S::kFU) ^ linear_swizzle<FEW32, S::kFU>(r);
+        funit[i] = (lane % S::kFU) ^ linear_swizzle<S::kFU, FEW32>(r);
     }
 #pragma unroll
     for (int i = 0; i < S::kManyLoads; ++i) {
         const int r = i * (kWave / S::kMU) + lane / S::kMU;
         moff[i] = (uint32_t)(r < mlast ? r : mlast) * (uint32_t)((size_t)p.K * (MANY32 ? 4 : 2));
-        munit[i] = (lane % S::kMU) ^ linear_swizzle<MANY32, S::kMU>(r);
+        munit[i] = (lane % S::kMU) ^ linear_swizzle<S::kMU, MANY32>(r);
     }
     const int full = DIRECT ? p.K / S::kBK : 0;
+    // steps that end behind K, and rows that begin between dwords, go through registers
+    u32x4 held_f[S::kFewLoads], held_m[S::kManyLoads];
+    auto fetch = [&](int st) {
+#pragma unroll
+        for (int i = 0; i < S::kManyLoads; ++i)
+            held_m[i] = row_unit<MANY32>(mbase + moff[i], st * S::kBK + munit[i] * (S::kBK / S::kMU), p.K);
+#pragma unroll
+        for (int i = 0; i < S::kFewLoads; ++i)
+            held_f[i] = row_unit<FEW32>(fbase + foff[i], st * S::kBK + funit[i] * (S::kBK / S::kFU), p.K);
+    };
+    auto put = [&](int slot) {
+        u32x4* const to = reinterpret_cast<u32x4*>(lds + w * (S::kRing * S::kSlot) + slot * S::kSlot) + lane;
+#pragma unroll
+        for (int i = 0; i < S::kManyLoads; ++i)
+            to[S::kFewBytes / 16 + i * kWave] = held_m[i];
+#pragma unroll
+        for (int i = 0; i < S::kFewLoads; ++i)
+            to[i * kWave] = held_f[i];
+    };
     auto stage = [&](int st, int slot) {
         const int to = w * (S::kRing * S::kSlot) + slot * S::kSlot;
         if (st < full) {
@@ -91,14 +111,8 @@ moe_linear_skinny_kernel(LinearArgs p, SkinnyPlan plan)
             for (int i = 0; i < S::kFewLoads; ++i)
                 load_to_lds16(fs, foff[i] + 16u * funit[i], lds0 + (uint32_t)(to + i * 1024));
         } else {
-            u32x4* const f16 = reinterpret_cast<u32x4*>(lds + to) + lane;
-            u32x4* const m16 = reinterpret_cast<u32x4*>(lds + to + S::kFewBytes) + lane;
-#pragma unroll
-            for (int i = 0; i < S::kManyLoads; ++i)
-                m16[i * kWave] = row_unit<MANY32>(mbase + moff[i], st * S::kBK + munit[i] * (S::kBK / S::kMU), p.K);
-#pragma unroll
-            for (int i = 0; i < S::kFewLoads; ++i)
-                f16[i * kWave] = row_unit<FEW32>(fbase + foff[i], st * S::kBK + funit[i] * (S::kBK / S::kFU), p.K);
+            fetch(st);
+            put(slot);
         }
     };
 
@@ -131,15 +145,27 @@ moe_linear_skinny_kernel(LinearArgs p, SkinnyPlan plan)
             stage(st0 + i * stride, i);
     int slot = 0;
     for (int i = 0; i < count; ++i) {
-        if (i + kAhead < count) {
-            wait_lds();                                       // the fragments of the step before, whose place is taken now
-            stage(st0 + (i + kAhead) * stride, slot == 0 ? kAhead : slot - 1);
-            wait_loads<kAhead * S::kLoads>();                 // all but the loads of the steps behind this one
+        const int free = slot == 0 ? kAhead : slot - 1;
+        const bool more = i + kAhead < count;
+        const int later = st0 + (i + kAhead) * stride;
+        if constexpr (DIRECT) {
+            if (more) {
+                wait_lds();                                   // the fragments of the step before, whose place is taken now
+                stage(later, free);
+                wait_loads<kAhead * S::kLoads>();             // all but the loads of the steps behind this one
+            } else {
+                wait_loads<0>();
+            }
+            wave_lds_fence();
+            compute(slot);
         } else {
-            wait_loads<0>();
+            if (more)
+                fetch(later);                                 // comes while this step is multiplied
+            wave_lds_fence();
+            compute(slot);
+            if (more)
+                put(free);
         }
-        wave_lds_fence();
-        compute(slot);
         slot = slot + 1 == S::kRing ? 0 : slot + 1;
     }
     // sums of the wavefronts: [wavefront][few][many]
@@ -185,10 +211,10 @@ hipError_t launch_skinny_shape(const LinearArgs& p, const SkinnyPlan& plan, hipS
 template <bool X32, bool W32>
 hipError_t launch_skinny(bool swapped, int rt, const LinearArgs& p, const SkinnyPlan& plan, hipStream_t s)
 {
-    const bool direct = p.K % (X32 ? 4 : 8) == 0 && p.K % (W32 ? 4 : 8) == 0;
+    const bool direct = (X32 && W32) || p.K % 2 == 0;
 #define MOED_SK(F, M, SW) \
     (direct ? (rt == 1 ? launch_skinny_shape<F, M, SW, true, 1>(p, plan, s) : launch_skinny_shape<F, M, SW, true, 2>(p, plan, s)) \
-            : (rt == 1 ? launch_skinny_shape<F, M, SW, false, 1>(p, plan, s) : launch_skinny_shape<F, M, SW, false, 2>(p, plan, s)))
+            : (rt == 1 ? launch_skinny_shape<F, M, SW, (F && M), 1>(p, plan, s) : launch_skinny_shape<F, M, SW, (F && M), 2>(p, plan, s)))
     return swapped ? MOED_SK(W32, X32, true) : MOED_SK(X32, W32, false);
 #undef MOED_SK
 }
