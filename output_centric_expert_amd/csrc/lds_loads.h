@@ -1,4 +1,4 @@
-// Loads from global memory straight to LDS, and reads of what they brought (the tiled products).
+// Loads from global memory straight to LDS, reads of what they brought, and the waits between.
 #pragma once
 
 #include "mx_device.h"
@@ -33,6 +33,13 @@ template <int N = 0>
 __device__ __forceinline__ void wait_lds()
 {
     asm volatile("s_waitcnt lgkmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// What this wavefront wrote to LDS is there for its other lanes.
+__device__ __forceinline__ void wave_lds_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 }
 
 // A workgroup's barrier and nothing else: what has to have come or gone before it is the caller's to wait for.

@@ -165,13 +165,6 @@ __device__ __forceinline__ void linear_products(const bf16x8 (&a)[A32 ? 3 : 1], 
                 acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[q - i], b[i], acc, 0, 0, 0);
 }
 
-// What this wavefront wrote to LDS is there for its other lanes.
-__device__ __forceinline__ void wave_lds_fence()
-{
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
-
 }  // namespace
 
 }  // namespace moed
