@@ -29,8 +29,8 @@ constexpr int kRouteWaves = 4;
 // Order-preserving map of a float32 to 32 bits; -0 as +0. No finite number or infinity maps to 0.
 __device__ __forceinline__ uint32_t order_key(float v)
 {
-    const uint32_t u = v == 0.0f ? 0u : __float_as_uint(v);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    const uint32_t u = __float_as_uint(v + 0.0f);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
 __device__ __forceinline__ float key_value(uint32_t key)
@@ -41,12 +41,12 @@ __device__ __forceinline__ float key_value(uint32_t key)
 // Key of a choice: 0 for NaN and -infinity.
 __device__ __forceinline__ uint32_t choice_key(float c) { return c > -__builtin_inff() ? order_key(c) : 0u; }
 
-// exp(x), |x| at most 150 (beyond, x counts as that: a float32 score is then 0 or 1): 2^n times Taylor's series of the
-// rest below ln(2)/2, whose first term left out is 2^-52 of it.
+// exp(x) for |x| up to 150 (callers clamp it there: a float32 score is 0 or 1 beyond): 2^n times Taylor's series of the
+// rest below ln(2)/2, whose first term left out is 2^-52 of it. n is rounded by adding 1.5 * 2^52, which leaves it in
+// the low word, and goes into the exponent by an addition: conversions have a quarter of the rate.
 __device__ __forceinline__ double exp64(double x)
 {
-    x = __builtin_fmin(__builtin_fmax(x, -150.0), 150.0);
-    const double n = __builtin_rint(x * 0x1.71547652b82fep+0);
+    const double shifted = __builtin_fma(x, 0x1.71547652b82fep+0, 0x1.8p52), n = shifted - 0x1.8p52;
     double r = __builtin_fma(-n, 0x1.62e42fefa39efp-1, x);
     r = __builtin_fma(-n, 0x1.abc9e3b39803fp-56, r);
     double p = 1.0 / 479001600.0;
@@ -62,15 +62,16 @@ __device__ __forceinline__ double exp64(double x)
     p = __builtin_fma(p, r, 0.5);
     p = __builtin_fma(p, r, 1.0);
     p = __builtin_fma(p, r, 1.0);
-    return __builtin_amdgcn_ldexp(p, (int)n);
+    const uint64_t u = __builtin_bit_cast(uint64_t, p);
+    const uint32_t high = (uint32_t)(u >> 32) + ((uint32_t)__builtin_bit_cast(uint64_t, shifted) << 20);
+    return __builtin_bit_cast(double, (uint64_t)high << 32 | (uint32_t)u);
 }
 
-// 1 / d for normal d: the hardware's estimate (2^-23 at least) and two steps of Newton's.
+// 1 / d for normal d: the hardware's estimate (2^-23 at least) and one step of third order.
 __device__ __forceinline__ double reciprocal64(double d)
 {
-    double y = __builtin_amdgcn_rcp(d);
-    y = __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
-    return __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
+    const double y = __builtin_amdgcn_rcp(d), e = __builtin_fma(-d, y, 1.0);
+    return __builtin_fma(y, __builtin_fma(e, e, e), y);
 }
 
 // v of another lane of the row of 16.
@@ -152,6 +153,9 @@ __device__ __forceinline__ void score_experts(const RouteArgs& p, size_t b, int 
     const int e0 = tl * NPL;
     const bool whole = NPL % 4 == 0 && e0 + NPL <= p.E;
     const size_t at = b * (size_t)p.E + e0;
+#pragma unroll
+    for (int t = 0; t < NPL; ++t)
+        bias[t] = 0.0f;
     if (whole) {
         if constexpr (NPL % 4 == 0) {
 #pragma unroll
@@ -170,22 +174,30 @@ __device__ __forceinline__ void score_experts(const RouteArgs& p, size_t b, int 
                         l[t + i] = u[i];
                 }
             }
+            if (p.bias) {
+#pragma unroll
+                for (int t = 0; t < NPL; t += 4) {
+                    const f32x4 u = ld_at4<false>(p.bias + e0 + t);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        bias[t + i] = u[i];
+                }
+            }
         }
     } else {
 #pragma unroll
         for (int t = 0; t < NPL; ++t) {
             l[t] = nan;
+            if (p.bias && e0 + t < p.E)
+                bias[t] = p.bias[e0 + t];
             if (e0 + t < p.E)
                 l[t] = BF16 ? bf16_val(static_cast<const uint16_t*>(p.logits)[at + t]) : static_cast<const float*>(p.logits)[at + t];
         }
     }
-#pragma unroll
-    for (int t = 0; t < NPL; ++t)
-        bias[t] = p.bias && e0 + t < p.E ? p.bias[e0 + t] : 0.0f;
     if (p.sigmoid) {
 #pragma unroll
         for (int t = 0; t < NPL; ++t)
-            x.score[t] = (float)reciprocal64(1.0 + exp64(-(double)l[t]));
+            x.score[t] = (float)reciprocal64(1.0 + exp64((double)__builtin_amdgcn_fmed3f(-l[t], -150.0f, 150.0f)));
     } else {
         float m = -__builtin_inff();
 #pragma unroll
@@ -195,7 +207,7 @@ __device__ __forceinline__ void score_experts(const RouteArgs& p, size_t b, int 
         double ex[NPL], sum = 0.0;
 #pragma unroll
         for (int t = 0; t < NPL; ++t) {
-            ex[t] = l[t] != l[t] ? 0.0 : l[t] == m ? 1.0 : exp64((double)l[t] - (double)m);
+            ex[t] = l[t] != l[t] ? 0.0 : l[t] == m ? 1.0 : exp64(__builtin_fmax((double)l[t] - (double)m, -150.0));
             sum += ex[t];
         }
         sum = reciprocal64(lanes_sum<L>(sum));
@@ -453,11 +465,12 @@ moe_route_scored_many_kernel(RouteArgs p)
 #pragma unroll
     for (int t = 0; t < NPL; ++t)
         scores[tl * NPL + t] = x.score[t];
-    // key * 2^11 + (2^11 - 1 - expert): whole numbers below 2^43, the lower expert the larger; 0 for none
+    // 2^52 + key * 2^11 + (2^11 - 1 - expert), by its bits: the lower expert is the larger
     double v[NPL];
 #pragma unroll
     for (int t = 0; t < NPL; ++t)
-        v[t] = x.key[t] ? __builtin_fma((double)x.key[t], 2048.0, (double)(2047 - (tl * NPL + t))) : 0.0;
+        v[t] = __builtin_bit_cast(double, (uint64_t)(0x43300000u | (x.key[t] >> 21)) << 32 |
+                                              (x.key[t] << 11 | (uint32_t)(2047 - (tl * NPL + t))));
     double best[kManyK];
     if constexpr (NPL > kManyK) {                             // the best eight of two eights
         sort_order<kManyK>(v, 0);
@@ -470,7 +483,7 @@ moe_route_scored_many_kernel(RouteArgs p)
         sort_order<NPL>(v, 0);
 #pragma unroll
         for (int i = 0; i < kManyK; ++i)
-            best[i] = i < kKeep ? v[i < kKeep ? i : 0] : 0.0;
+            best[i] = i < kKeep ? v[i < kKeep ? i : 0] : 0x1p52;
     }
     merge_lane<kXor1>(best);
     merge_lane<kXor2>(best);
@@ -479,8 +492,8 @@ moe_route_scored_many_kernel(RouteArgs p)
     int chosen = 0;
 #pragma unroll
     for (int j = 0; j < kManyK; ++j) {
-        const uint64_t u = (uint64_t)best[j];
-        if (j < p.k && u != 0) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, best[j]);
+        if (j < p.k && (u & 0xFFFFFFFFFF800ull) != 0) {       // a key
             chosen = j + 1;
             if (tl == j)
                 picks[slot][j] = 2047 - (int)(u & 2047);
