@@ -350,6 +350,7 @@ def _opt(t, name, dtypes, shape, dev):
 
 
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = torch.cuda.current_device
 
 
 def _raw_stream(stream, dev):
@@ -597,23 +598,43 @@ def moe_linear_workspace_bytes(B: int, K: int, N: int, x_dtype=torch.bfloat16, w
     return int(load().moe_linear_workspace_bytes(B, K, N, _DT[x_dtype], _DT[w_dtype]))
 
 
+def _operand(t, name, shape, dev):
+    """(address, moed_dtype) of a contiguous bfloat16 or float32 tensor of `shape` on device index `dev`."""
+    try:
+        if t.get_device() == dev and t.shape == shape and t.is_contiguous():
+            return t.data_ptr(), _DT[t.dtype]
+    except (AttributeError, KeyError):
+        pass
+    _refuse(t, name, _F, shape, dev)
+
+
+def _made(shape, dtype, x, stream):
+    """(result made here, address, moed_dtype)."""
+    code = _DT.get(dtype)
+    if code is None:
+        raise TypeError(f"out_dtype: unsupported type {dtype}")
+    t = x.new_empty(shape, dtype=dtype) if stream is None else _new(shape, dtype, x, stream)
+    return t, t.data_ptr(), code
+
+
 def moe_linear(x, w, bias=None, activation=None, residual=None, out=None, out_dtype=torch.bfloat16, workspace=None,
                stream=None):
     """Dense product with an epilogue: returns out [B, N] = act(x @ w.T + bias) + residual, rounded once.
 
     x [B, K], w [N, K], bias [N] and residual [B, N] are bfloat16 or float32 each. activation: None, "silu", "gelu",
     "gelu_tanh", "relu", "sigmoid" or "tanh". residual may be out, for an update in place."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("expected x [B, K] and w [N, K]")
-    B, K = x.shape
+    B, K = size = x.shape
     N = w.shape[0]
-    act = _choice(_ACT, activation, "activation")
-    xp, wp = _arg(x, "x", _F, None, dev), _arg(w, "w", _F, (N, K), dev)
-    bp, rp = _opt(bias, "bias", _F, (N,), dev), _opt(residual, "residual", _F, (B, N), dev)
-    out, op = _result(out, "out", _F, (B, N), dev, out_dtype, x, stream)
+    act = _ACT[activation] if activation in _ACT else _choice(_ACT, activation, "activation")
+    xp, xd = _operand(x, "x", size, dev)
+    wp, wd = _operand(w, "w", (N, K), dev)
+    bp, bd = (None, 0) if bias is None else _operand(bias, "bias", (N,), dev)
+    rp, rd = (None, 0) if residual is None else _operand(residual, "residual", (B, N), dev)
+    out, op, od = _made((B, N), out_dtype, x, stream) if out is None else (out, *_operand(out, "out", (B, N), dev))
     lib = load()
-    xd, wd = _DT[x.dtype], _DT[w.dtype]
     sp = sb = 0
     if workspace is not None:
         sp, sb = _arg(workspace, "workspace", _U8, None, dev), workspace.numel()
@@ -622,9 +643,7 @@ def moe_linear(x, w, bias=None, activation=None, residual=None, out=None, out_dt
         if need:
             workspace = _new((need,), torch.uint8, x, stream)
             sp, sb = workspace.data_ptr(), need
-    st = lib.moe_linear(xp, xd, wp, wd, bp, _DT[bias.dtype] if bias is not None else 0, act, rp,
-                        _DT[residual.dtype] if residual is not None else 0, op, _DT[out.dtype], B, K, N, sp, sb,
-                        _raw_stream(stream, dev))
+    st = lib.moe_linear(xp, xd, wp, wd, bp, bd, act, rp, rd, op, od, B, K, N, sp, sb, _raw_stream(stream, dev))
     _check(st, "moe_linear")
     return out
 
@@ -639,19 +658,28 @@ def moe_route_scored(logits, k: int, score: str = "sigmoid", bias=None, n_group:
     topk_group of n_group groups whose largest ("max"), or two largest ("top2"), of these are worth most; their
     weights are the scores without the bias, divided by their sum with renormalize, times routed_scale. Shared slots
     get ids E, E+1, ... and weight 1."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     if logits.dim() != 2:
         raise ValueError("logits: expected shape [B, E]")
-    B, E = logits.shape
-    kt = k + n_shared
-    lp, bp = _arg(logits, "logits", _F, None, dev), _opt(bias, "bias", _F32, (E,), dev)
+    B, E = size = logits.shape
+    lp, ld = _operand(logits, "logits", size, dev)
+    bp = None if bias is None else _arg(bias, "bias", _F32, (E,), dev)
     sc, gs = _choice(_SCORE, score, "score"), _choice(_GROUP, group_score, "group_score")
-    if min(k, n_shared) < 0:
+    if k < 0 or n_shared < 0:
         raise ValueError("k and n_shared are not negative")
-    ids, ip = _result(ids, "ids", _I32, (B, kt), dev, torch.int32, logits, stream)
-    w, wp = _result(w, "w", _F32, (B, kt), dev, torch.float32, logits, stream)
-    st = load().moe_route_scored(lp, _DT[logits.dtype], bp, sc, n_group, topk_group, gs, renormalize, B, E, k, n_shared,
-                                 routed_scale, ip, wp, _raw_stream(stream, dev))
+    shape = (B, k + n_shared)
+    if ids is None:
+        ids = _new(shape, torch.int32, logits, stream)
+        ip = ids.data_ptr()
+    else:
+        ip = _arg(ids, "ids", _I32, shape, dev)
+    if w is None:
+        w = _new(shape, torch.float32, logits, stream)
+        wp = w.data_ptr()
+    else:
+        wp = _arg(w, "w", _F32, shape, dev)
+    st = load().moe_route_scored(lp, ld, bp, sc, n_group, topk_group, gs, renormalize, B, E, k, n_shared, routed_scale, ip,
+                                 wp, _raw_stream(stream, dev))
     _check(st, "moe_route_scored")
     return ids, w
 
@@ -669,53 +697,60 @@ def moe_post_norm(y, residual, post_gain=None, post_eps: float = 1e-6, gate=None
     y is [B, H]; with position int32 [B, k] and topk_w float32 [B, k] it is the experts' rows [R, H], and their weighted
     sum (moe_combine's) is taken. gate: one number a token [B, 1], a channel [H] or [1, H], or each [B, H]; gate_act:
     None, "sigmoid" or "tanh". Give the residual as residual_out for an update in place."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     if y.dim() != 2 or residual.dim() != 2:
         raise ValueError("expected y [B, H] (or [R, H] with position) and residual [B, H]")
-    B, H = residual.shape
-    rp, rd = _arg(residual, "residual", _F, None, dev), residual.dtype
-    pp = tp = gp = None
-    R = k = shape = 0
+    B, H = size = residual.shape
+    rp, rd = _operand(residual, "residual", size, dev)
+    pp = tp = None
+    R = k = 0
     if position is not None:
         if topk_w is None or position.dim() != 2:
             raise ValueError("position: expected shape [B, k], with topk_w")
         R, k = y.shape[0], position.shape[1]
-        yp = _arg(y, "y", _F, (R, H), dev)
+        yp, yd = _operand(y, "y", (R, H), dev)
         pp, tp = _arg(position, "position", _I32, (B, k), dev), _arg(topk_w, "topk_w", _F32, (B, k), dev)
     elif topk_w is not None:
         raise ValueError("topk_w needs position")
     else:
-        yp = _arg(y, "y", _F, (B, H), dev)
+        yp, yd = _operand(y, "y", size, dev)
+    act = _GATE_ACT[gate_act] if gate_act in _GATE_ACT else _choice(_GATE_ACT, gate_act, "gate_act")
     if gate is not None:
         gs = tuple(gate.shape) if isinstance(gate, torch.Tensor) else None
-        shape = 3 if gs == (B, H) else 2 if gs in ((H,), (1, H)) else 1
-        gp = _arg(gate, "gate", _F, gs if shape > 1 else (B, 1), dev)
-    elif gate_act is not None:
+        kind = 3 if gs == (B, H) else 2 if gs == (H,) or gs == (1, H) else 1
+        gp, gd = _operand(gate, "gate", gs if kind > 1 else (B, 1), dev)
+    elif act:
         raise ValueError("gate_act needs a gate")
-    act = _choice(_GATE_ACT, gate_act, "gate_act")
+    else:
+        gp, gd, kind = None, 0, 0
     if quantize and H % 32:
         raise ValueError("quantize needs H to be a multiple of 32")
-    residual_out, rop = _result(residual_out, "residual_out", (rd,), (B, H), dev, rd, residual, stream)
-    op = qp = sp = None
+    op = qp = sp = gain_p = None
+    od = gain_d = 0
     if gain is None:
         if out is not None or quantize or out_q is not None or out_s is not None:
             raise ValueError("out, quantize, out_q and out_s need a gain")
     else:
-        if out is not None or out_dtype is not None:
-            out, op = _result(out, "out", _F, (B, H), dev, out_dtype, residual, stream)
+        gain_p, gain_d = _operand(gain, "gain", (H,), dev)
+        if out is not None:
+            op, od = _operand(out, "out", size, dev)
+        elif out_dtype is not None:
+            out, op, od = _made(size, out_dtype, residual, stream)
+        elif not quantize:
+            raise ValueError("gain needs an output: out_dtype or quantize")
         if quantize:
-            out_q, qp = _result(out_q, "out_q", _U8, (B, H), dev, torch.uint8, residual, stream)
+            out_q, qp = _result(out_q, "out_q", _U8, size, dev, torch.uint8, residual, stream)
             out_s, sp = _result(out_s, "out_s", _U8, (B, H // 32), dev, torch.uint8, residual, stream)
         elif out_q is not None or out_s is not None:
             raise ValueError("out_q and out_s need quantize=True")
-        elif out is None:
-            raise ValueError("gain needs an output: out_dtype or quantize")
-    st = load().moe_post_norm(
-        yp, _DT[y.dtype], R, pp, tp, k, _opt(post_gain, "post_gain", _F, (H,), dev),
-        _DT[post_gain.dtype] if post_gain is not None else 0, post_eps, gp, _DT[gate.dtype] if gate is not None else 0,
-        shape, act, scale, rp, _DT[rd], residual_scale, rop, _opt(gain, "gain", _F, (H,), dev),
-        _DT[gain.dtype] if gain is not None else 0, eps, op, _DT[out.dtype] if out is not None else 0, qp, sp, B, H,
-        _raw_stream(stream, dev))
+    if residual_out is None:
+        residual_out = _new(size, residual.dtype, residual, stream)
+        rop = residual_out.data_ptr()
+    else:
+        rop = _arg(residual_out, "residual_out", (residual.dtype,), size, dev)
+    post_p, post_d = (None, 0) if post_gain is None else _operand(post_gain, "post_gain", (H,), dev)
+    st = load().moe_post_norm(yp, yd, R, pp, tp, k, post_p, post_d, post_eps, gp, gd, kind, act, scale, rp, rd,
+                              residual_scale, rop, gain_p, gain_d, eps, op, od, qp, sp, B, H, _raw_stream(stream, dev))
     _check(st, "moe_post_norm")
     return out, residual_out, out_q, out_s
 
