@@ -492,8 +492,8 @@ typedef enum {
  * A row's low bits can differ between calls of different sizes.
  * workspace: at least moe_linear_workspace_bytes(...) bytes (0 for invalid
  * arguments), 16-byte aligned; NULL where that is 0.
- * Limits (MOED_ERR_SHAPE): 1 <= K, N < 2^20; K*N below 2^32; B*K and B*N below
- * 2^40. x, w, residual and out are 16-byte aligned, bias by its element
+ * Limits (MOED_ERR_SHAPE): 1 <= K, N < 2^20; K*N below 2^32; B*K below 2^40,
+ * B*N below 2^38. x, w, residual and out are 16-byte aligned, bias by its element
  * (MOED_ERR_ALIGN). B = 0 launches nothing.
  */
 size_t moe_linear_workspace_bytes(int B, int K, int N, int x_dtype, int w_dtype);

@@ -24,7 +24,7 @@ constexpr int kMaxRowLength = 1 << 20;
 bool linear_ok(int B, int K, int N)
 {
     return B >= 0 && B < moed::kMaxTokens && K >= 1 && N >= 1 && K < kMaxRowLength && N < kMaxRowLength &&
-           (long long)K * N < (1LL << 32) && (long long)B * K < (1LL << 40) && (long long)B * N < (1LL << 40);
+           (long long)K * N < (1LL << 32) && (long long)B * K < (1LL << 40) && (long long)B * N < (1LL << 38);
 }
 
 }  // namespace

@@ -1,8 +1,5 @@
 // Dense product with bias, activation and residual: out[b][n] = act(x[b] . w[n] + bias[n]) + residual[b][n].
-//
-// A wavefront owns NW weight rows and RB rows of x. Its lanes take pieces of 8 neighbouring k, so that a load of a row
-// is contiguous over the wavefront; products are summed in float32 per lane and then over the lanes. KS wavefronts of
-// a workgroup share a row's k where there are too few rows to fill the chip.
+// The choice of a kernel, the kernel of a single row of x, and the sum of a product whose k was split.
 #include "linear_skinny.h"
 #include "linear_tiled.h"
 
@@ -14,67 +11,32 @@ constexpr int kDotWaves = 4;
 
 }  // namespace
 
-template <bool XBF16, bool WBF16, int RB, int NW, int KS>
+// One row of x. A workgroup's four wavefronts share an output's k; their lanes take pieces of 8 neighbouring values, so that
+// a load of a row is contiguous over the wavefront. Bound by the weights' way from memory (4096 x 4096 bfloat16 8.7 us,
+// 3.9 TB/s, of which the launch is 2) and, with few outputs, by one round trip (2048 -> 128 float32: 3.4-4.2 us, the
+// kernel of few rows 6.2: it has 8 workgroups for it, this one 128).
+template <bool XBF16, bool WBF16>
 __global__ void __launch_bounds__(kDotWaves * kWave)
-moe_linear_dot_kernel(LinearArgs p, int n_blocks)
+moe_linear_dot_kernel(LinearArgs p)
 {
-    constexpr int kParts = kDotWaves / KS;        // wavefronts with weight rows of their own
-    __shared__ float part[kDotWaves][RB * NW];
-    const int lane = threadIdx.x % kWave, w = threadIdx.x / kWave, ks = w % KS;
-    const size_t b0 = (size_t)(blockIdx.x / (unsigned)n_blocks) * RB;
-    const int block_n = (int)(blockIdx.x % (unsigned)n_blocks) * (NW * kParts);
-    const int n0 = block_n + w / KS * NW;
-    float acc[RB][NW];
+    __shared__ float part[kDotWaves];
+    const int lane = threadIdx.x % kWave, w = threadIdx.x / kWave, n = blockIdx.x;
+    const size_t row = (size_t)n * (size_t)p.K;
+    float sum = 0.0f;
+    for (int k = threadIdx.x * 8; k < p.K; k += kDotWaves * kWave * 8) {
+        float wv[8], xv[8];
+        load_any<WBF16, false>(p.w, row + k, p.K - k, wv);
+        load_any<XBF16, false>(p.x, (size_t)k, p.K - k, xv);
 #pragma unroll
-    for (int r = 0; r < RB; ++r)
-#pragma unroll
-        for (int n = 0; n < NW; ++n)
-            acc[r][n] = 0.0f;
-    // rows behind the last repeat it
-    size_t wrow[NW], xrow[RB];
-#pragma unroll
-    for (int n = 0; n < NW; ++n)
-        wrow[n] = (size_t)(n0 + n < p.N ? n0 + n : p.N - 1) * (size_t)p.K;
-#pragma unroll
-    for (int r = 0; r < RB; ++r)
-        xrow[r] = (b0 + r < (size_t)p.B ? b0 + r : (size_t)p.B - 1) * (size_t)p.K;
-    for (int k = (ks * kWave + lane) * 8; k < p.K; k += KS * kWave * 8) {
-        float wv[NW][8];
-#pragma unroll
-        for (int n = 0; n < NW; ++n)
-            load_any<WBF16, false>(p.w, wrow[n] + k, p.K - k, wv[n]);
-#pragma unroll
-        for (int r = 0; r < RB; ++r) {
-            float xv[8];
-            load_any<XBF16, false>(p.x, xrow[r] + k, p.K - k, xv);
-#pragma unroll
-            for (int n = 0; n < NW; ++n)
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    acc[r][n] = __builtin_fmaf(xv[i], wv[n][i], acc[r][n]);
-        }
+        for (int i = 0; i < 8; ++i)
+            sum = __builtin_fmaf(xv[i], wv[i], sum);
     }
-#pragma unroll
-    for (int r = 0; r < RB; ++r)
-#pragma unroll
-        for (int n = 0; n < NW; ++n) {
-            const float v = wave_sum(acc[r][n]);
-            if (lane == 0)
-                part[w][r * NW + n] = v;
-        }
+    sum = wave_sum(sum);
+    if (lane == 0)
+        part[w] = sum;
     __syncthreads();
-    const int i = threadIdx.x;
-    if (i >= kParts * RB * NW)
-        return;
-    const int at = i % (RB * NW), from = i / (RB * NW);
-    float v = 0.0f;
-#pragma unroll
-    for (int q = 0; q < KS; ++q)
-        v += part[from * KS + q][at];
-    const size_t b = b0 + at / NW;
-    const int n = block_n + from * NW + at % NW;
-    if (b < (size_t)p.B && n < p.N)
-        linear_store(p, v, b, n);
+    if (threadIdx.x == 0)
+        linear_store(p, (part[0] + part[1]) + (part[2] + part[3]), 0, n);
 }
 
 // The sums of a product whose k was split, added in the order of the splits, and the epilogue. V neighbouring outputs of a
@@ -116,7 +78,6 @@ moe_linear_join_kernel(LinearArgs p, const float* partial, int splits, unsigned 
 
 namespace {
 
-constexpr int kDotRows = 1;                       // up to here the rows are multiplied without matrix instructions
 constexpr int kSkinnyTiles = 400;                 // tiles up to which a product of more than 16 rows is a skinny one
 
 struct Choice {
@@ -140,7 +101,7 @@ Choice choose(int B, int K, int N, bool x_bf16, bool w_bf16)
     c.tile = c.rt = 0;
     c.splits = 1;
     c.swapped = false;
-    if (B <= kDotRows) {
+    if (B == 1) {
         c.kind = Choice::dot;
         return c;
     }
@@ -202,15 +163,6 @@ size_t linear_workspace(int B, int K, int N, bool x_bf16, bool w_bf16)
 
 namespace {
 
-template <bool X, bool W, int RB, int NW, int KS>
-hipError_t launch_dot_shape(const LinearArgs& p, hipStream_t s)
-{
-    const int per = NW * (kDotWaves / KS), nb = (p.N + per - 1) / per;
-    const unsigned grid = (unsigned)((long long)nb * ((p.B + RB - 1) / RB));
-    hipLaunchKernelGGL((moe_linear_dot_kernel<X, W, RB, NW, KS>), dim3(grid), dim3(kDotWaves * kWave), 0, s, p, nb);
-    return hipGetLastError();
-}
-
 hipError_t launch_join(const LinearArgs& p, const float* partial, int splits, hipStream_t s)
 {
     // below, single outputs fill the chip sooner
@@ -227,7 +179,8 @@ hipError_t launch_join(const LinearArgs& p, const float* partial, int splits, hi
 template <bool X, bool W>
 hipError_t launch_dot(const LinearArgs& p, hipStream_t s)
 {
-    return launch_dot_shape<X, W, 1, 1, 4>(p, s);
+    hipLaunchKernelGGL((moe_linear_dot_kernel<X, W>), dim3((unsigned)p.N), dim3(kDotWaves * kWave), 0, s, p);
+    return hipGetLastError();
 }
 
 }  // namespace

@@ -8,7 +8,8 @@ namespace {
 
 constexpr TileCost kTiles[] = {
     {256, 128, 32, 2.40f, 0.00f},
-    {64, 64, 32, 0.78f, 1.05f}};
+    {64, 64, 32, 0.78f, 1.05f},
+    {64, 64, 64, 1.14f, 0.00f}};
 
 }  // namespace
 
@@ -23,8 +24,9 @@ bool linear_cost_f32(int tile, TileCost* cost)
 hipError_t launch_linear_f32(int tile, const LinearArgs& p, const LinearPlan& plan, hipStream_t s)
 {
     switch (tile) {
-    case 0: return launch_linear_tile<true, true, 4, 4, 4, 2, 2>(p, plan, s);
-    case 1: return launch_linear_tile<true, true, 2, 2, 2, 2, 2>(p, plan, s);
+    case 0: return launch_linear_tile<true, true, 4, 4, 4, 2, 2, 32>(p, plan, s);
+    case 1: return launch_linear_tile<true, true, 2, 2, 2, 2, 2, 32>(p, plan, s);
+    case 2: return launch_linear_tile<true, true, 2, 1, 2, 4, 2>(p, plan, s);
     default: return hipErrorInvalidValue;
     }
 }

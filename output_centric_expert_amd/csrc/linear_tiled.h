@@ -107,11 +107,11 @@ struct LinearSide {
 // In the place of a number of buffers: three of x and two of w.
 constexpr int kDeep = 0;
 
-template <bool XF32, bool WF32, bool DIRECT, int RT, int NT, int WR, int WN, int RING>
+template <bool XF32, bool WF32, bool DIRECT, int RT, int NT, int WR, int WN, int RING, int BK>
 struct LinearShape {
     static constexpr int kWaves = WR * WN, kThreads = kWaves * kWave;
     static constexpr int kBM = 16 * RT * WR, kBN = 16 * NT * WN;          // rows of x and of w in a tile
-    static constexpr int kBK = XF32 && WF32 ? 32 : 64;
+    static constexpr int kBK = BK;
     using X = LinearSide<XF32, DIRECT, kBM, kThreads, kBK>;
     using W = LinearSide<WF32, DIRECT, kBN, kThreads, kBK>;
     static constexpr int kBuffer = X::kBytes + W::kBytes;
@@ -126,11 +126,11 @@ struct LinearShape {
 }  // namespace
 
 // DIRECT: no bfloat16 rows of odd K.
-template <bool XF32, bool WF32, bool DIRECT, int RT, int NT, int WR, int WN, int RING>
+template <bool XF32, bool WF32, bool DIRECT, int RT, int NT, int WR, int WN, int RING, int BK>
 __global__ void __launch_bounds__(WR * WN * kWave)
 moe_linear_tiled_kernel(LinearArgs p, LinearPlan plan)
 {
-    using S = LinearShape<XF32, WF32, DIRECT, RT, NT, WR, WN, RING>;
+    using S = LinearShape<XF32, WF32, DIRECT, RT, NT, WR, WN, RING, BK>;
     using X = typename S::X;
     using W = typename S::W;
     extern __shared__ __align__(16) uint8_t lds[];
@@ -439,28 +439,29 @@ struct TileCost {
     float alone, paired;    // with one workgroup a CU, and with two (0: there is no room for two)
 };
 
-template <bool XF32, bool WF32, bool DIRECT, int RT, int NT, int WR, int WN, int RING>
+template <bool XF32, bool WF32, bool DIRECT, int RT, int NT, int WR, int WN, int RING, int BK>
 hipError_t launch_linear_shape(const LinearArgs& p, const LinearPlan& plan, hipStream_t s)
 {
-    using S = LinearShape<XF32, WF32, DIRECT, RT, NT, WR, WN, RING>;
+    using S = LinearShape<XF32, WF32, DIRECT, RT, NT, WR, WN, RING, BK>;
     static_assert(16 * NT <= kWave, "a wavefront stores whole rows of its outputs");
-    const void* f = reinterpret_cast<const void*>(&moe_linear_tiled_kernel<XF32, WF32, DIRECT, RT, NT, WR, WN, RING>);
+    const void* f = reinterpret_cast<const void*>(&moe_linear_tiled_kernel<XF32, WF32, DIRECT, RT, NT, WR, WN, RING, BK>);
     if (S::kLds > 49152)
         if (hipError_t e = set_max_dynamic_lds(f, S::kLds))
             return e;
     const unsigned grid = (unsigned)((long long)plan.n_blocks * plan.m_blocks * plan.splits);
-    hipLaunchKernelGGL((moe_linear_tiled_kernel<XF32, WF32, DIRECT, RT, NT, WR, WN, RING>), dim3(grid), dim3(S::kThreads), S::kLds, s, p,
+    hipLaunchKernelGGL((moe_linear_tiled_kernel<XF32, WF32, DIRECT, RT, NT, WR, WN, RING, BK>), dim3(grid), dim3(S::kThreads), S::kLds, s, p,
                        plan);
     return hipGetLastError();
 }
 
-template <bool XF32, bool WF32, int RT, int NT, int WR, int WN, int RING>
+// RING: buffers of a step, or kDeep; BK: values of k in a step.
+template <bool XF32, bool WF32, int RT, int NT, int WR, int WN, int RING, int BK = 64>
 hipError_t launch_linear_tile(const LinearArgs& p, const LinearPlan& plan, hipStream_t s)
 {
     if ((XF32 && WF32) || p.K % 2 == 0)
-        return launch_linear_shape<XF32, WF32, true, RT, NT, WR, WN, RING>(p, plan, s);
+        return launch_linear_shape<XF32, WF32, true, RT, NT, WR, WN, RING, BK>(p, plan, s);
     if constexpr (!(XF32 && WF32))
-        return launch_linear_shape<XF32, WF32, false, RT, NT, WR, WN, 2>(p, plan, s);
+        return launch_linear_shape<XF32, WF32, false, RT, NT, WR, WN, 2, BK>(p, plan, s);
 }
 
 // One source file per pair of types. cost: of tile number i, false behind the last.

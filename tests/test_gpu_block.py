@@ -69,7 +69,14 @@ def check_linear(x, w, bias, act, residual, out):
 SIZES = [(1, 1, 1), (1, 2048, 128), (1, 7168, 256), (2, 33, 5), (3, 1111, 777), (4, 8, 4096), (5, 4096, 1), (7, 100, 300),
          (8, 2048, 512), (9, 512, 16), (16, 7168, 256), (17, 63, 65), (31, 2049, 130), (32, 4096, 1024), (33, 64, 33),
          (64, 7168, 256), (65, 200, 257), (127, 1000, 96), (128, 128, 128), (200, 20000, 40), (256, 256, 512), (300, 1, 300),
-         (1000, 1111, 777), (513, 4104, 520), (2048, 96, 8), (2500, 7, 3), (1024, 1024, 1024), (4096, 520, 264), (4100, 264, 4100), (4100, 77, 4099)]
+         (1000, 1111, 777), (513, 4104, 520), (2048, 96, 8), (2500, 7, 3), (1024, 1024, 1024), (4096, 520, 264), (4100, 264, 4100), (4100, 77, 4099),
+         # each tile with K even and odd, with k whole and split, steps that end behind K and that do not
+         (4090, 712, 4093), (4090, 711, 4093), (4096, 256, 4096), (3161, 37, 2629), (4272, 34, 899), (3692, 33, 1028),
+         (2052, 2877, 900), (3422, 34, 546), (647, 33, 2967), (4107, 2212, 35), (3291, 2871, 34), (34, 34, 3285), (33, 33, 3425),
+         (36, 998, 3244), (3225, 1189, 33), (2369, 33, 1717), (133, 2816, 3586), (3943, 2765, 130), (3491, 850, 33),
+         (36, 887, 3461), (2299, 35, 1812), (2765, 1296, 641), (808, 1319, 2466), (3427, 884, 33), (34, 971, 3354),
+         (4340, 2106, 71), (259, 37, 3333), (35, 604, 3665), (33, 613, 3401), (3271, 40, 37), (34, 1292, 3557), (36, 1325, 3674),
+         (18, 1492, 20), (18, 1561, 19), (19, 1724, 18), (19, 1963, 18), (20, 890, 18), (21, 789, 18)]
 
 
 @pytest.mark.parametrize("B,K,N", SIZES)
@@ -169,6 +176,47 @@ def test_linear_far_values(B, power):
     assert ((a - b).abs().double() <= 256 * 2 * U * (x.double().abs() @ w.double().abs().T)).all()
 
 
+@pytest.mark.parametrize("B,K,N", [(1, 77, 5), (5, 77, 40), (40, 1111, 40), (40, 65, 7), (300, 77, 500), (300, 1028, 500),
+                                   (300, 1029, 500), (2000, 33, 700), (4090, 201, 4090)])
+@pytest.mark.parametrize("x_type,w_type", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16"), ("f32", "f32")])
+def test_linear_reads_and_writes_nothing_behind(B, K, N, x_type, w_type):
+    """NaN in front of and behind x, w, bias and residual changes nothing; what lies around out stays."""
+    g = gen(B + K + N)
+
+    def inside(t):
+        buf = torch.full((t.numel() + 1024,), float("nan"), device="cuda", dtype=t.dtype)
+        buf[512:512 + t.numel()] = t.reshape(-1)
+        return buf[512:512 + t.numel()].view(t.shape)
+
+    x, w, b, r = randn(g, B, K).to(TYPES[x_type]), randn(g, N, K).to(TYPES[w_type]), randn(g, N), randn(g, B, N)
+    for dt in TYPES.values():
+        ref = md.moe_linear(x, w, bias=b, residual=r.to(dt), out_dtype=dt)
+        buf = torch.full((B * N + 1024,), 7.0, device="cuda", dtype=dt)
+        out = buf[512:512 + B * N].view(B, N)
+        md.moe_linear(inside(x), inside(w), bias=inside(b), residual=inside(r.to(dt)), out=out)
+        assert torch.equal(bits(out), bits(ref)) and (buf[:512] == 7).all() and (buf[512 + B * N:] == 7).all()
+
+
+@pytest.mark.parametrize("B,K,N,x_type,w_type", [(300000, 8192, 16, "bf16", "bf16"), (300000, 8192, 40, "bf16", "bf16"),
+                                                 (300000, 8190, 300, "bf16", "f32"), (150000, 8191, 40, "f32", "bf16"),
+                                                 (40, 4096, 600000, "bf16", "bf16"), (3, 4097, 600000, "bf16", "bf16"),
+                                                 (1, 4097, 600000, "bf16", "f32"), (9000, 64, 300000, "bf16", "bf16"),
+                                                 (5, (1 << 20) - 1, 40, "bf16", "f32"), (300, (1 << 20) - 3, 300, "bf16", "bf16")])
+def test_linear_past_32_bits(B, K, N, x_type, w_type):
+    """Operands and outputs past 4 GiB, rows of a million values: outputs at the ends and at random places."""
+    g = gen(11)
+    x = torch.empty(B, K, device="cuda", dtype=TYPES[x_type])
+    w = torch.empty(N, K, device="cuda", dtype=TYPES[w_type])
+    for t in (x, w):
+        for part in t.split(1 << 14):
+            part.copy_(torch.randint(-2, 3, part.shape, generator=g, device="cuda"))
+    out = md.moe_linear(x, w, out_dtype=torch.bfloat16 if B * N > 1 << 30 else torch.float32)
+    rows = torch.cat([torch.arange(min(B, 3)), torch.arange(max(0, B - 3), B), torch.randint(0, B, (40,))]).unique().cuda()
+    cols = torch.cat([torch.arange(min(N, 3)), torch.arange(max(0, N - 3), N), torch.randint(0, N, (200,))]).unique().cuda()
+    ref = x[rows].double() @ w[cols].double().T               # whole numbers below 2^24: exact
+    assert torch.equal(out[rows][:, cols], ref.to(out.dtype))
+
+
 def test_linear_repeats():
     """The same call gives the same bits."""
     g = gen(5)
@@ -196,13 +244,11 @@ def test_linear_empty_and_refusals():
         md.moe_linear(x, w[:, :63])
     with pytest.raises(md.MoedError):                         # an address between 16-byte borders
         md.moe_linear(torch.ones(257, device="cuda")[1:].view(4, 64), w)
-    big = 1 << 16
     need = md.moe_linear_workspace_bytes(64, 7168, 256, torch.bfloat16, torch.float32)
     if need:
         with pytest.raises(md.MoedError):
             md.moe_linear(torch.ones(64, 7168, device="cuda").bfloat16(), torch.ones(256, 7168, device="cuda"),
                           workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
-    del big
 
 
 # ---------------------------------------------------------------------------- route
@@ -318,6 +364,25 @@ def test_route_scored_special_values(score, B):
                 for renorm in (False, True):
                     check_route(x, k, score, b, G, take, gs, renorm, 1, 0.5)
                     check_route(x, k, score, b, G, G, gs, renorm)
+
+
+def test_route_scored_many_tokens():
+    """As many tokens as the limit lets through, logits past 4 GiB."""
+    B, E = (1 << 22) - 1, 511
+    logits = torch.empty(B, E, device="cuda")
+    for part in logits.split(1 << 18):
+        part.normal_(generator=gen(part.data_ptr() % 1000))
+    for k, G, take in ((8, 1, 1), (2, 7, 3)):
+        ids, w = md.moe_route_scored(logits, k, n_group=G, topk_group=take)
+        for rows in (slice(0, 40), slice(B - 40, B), slice(2103000, 2103040)):
+            rid, rw = route_ref(logits[rows].cpu().numpy(), k, "sigmoid", None, G, take, "top2", True, 0, 1.0)
+            assert np.array_equal(ids[rows].cpu().numpy(), rid) and np.allclose(w[rows].cpu().numpy(), rw, rtol=2 * U, atol=0)
+    del logits
+    logits = randn(gen(4), (1 << 22) - 1, 200)                # the kernel for many tokens, an odd count of them
+    ids, w = md.moe_route_scored(logits, 8, n_group=8, topk_group=4)
+    for rows in (slice(0, 40), slice((1 << 22) - 41, (1 << 22) - 1)):
+        rid, rw = route_ref(logits[rows].cpu().numpy(), 8, "sigmoid", None, 8, 4, "top2", True, 0, 1.0)
+        assert np.array_equal(ids[rows].cpu().numpy(), rid) and np.allclose(w[rows].cpu().numpy(), rw, rtol=2 * U, atol=0)
 
 
 def test_route_scored_is_route():
@@ -454,6 +519,48 @@ def test_post_norm_of_rows(B, H, k, y_type, r_type):
         keep = torch.arange(B, device="cuda") != B // 2
         assert o3[B // 2].isnan().all() and res3[B // 2].isnan().all()
         assert torch.equal(bits(o3[keep]), bits(out[keep])) and torch.equal(bits(res3[keep]), bits(res[keep]))
+
+
+@pytest.mark.parametrize("H", [3, 31, 777, 1111, 4095, 4104, 8195, 20001])
+def test_post_norm_reads_and_writes_nothing_behind(H):
+    """NaN around the inputs changes nothing; what lies around the outputs stays."""
+    g = gen(H)
+
+    def inside(t):
+        buf = torch.full((t.numel() + 1024,), float("nan"), device="cuda", dtype=t.dtype)
+        buf[512:512 + t.numel()] = t.reshape(-1)
+        return buf[512:512 + t.numel()].view(t.shape)
+
+    for dt in TYPES.values():
+        y, r, gain, gate = (randn(g, *s).to(dt) for s in ((5, H), (5, H), (H,), (5, H)))
+        a = md.moe_post_norm(y, r, post_gain=gain, gate=gate, gain=gain, out_dtype=dt)
+        bufs = [torch.full((5 * H + 1024,), 7.0, device="cuda", dtype=dt) for _ in range(2)]
+        out, res = (t[512:512 + 5 * H].view(5, H) for t in bufs)
+        md.moe_post_norm(inside(y), inside(r), post_gain=inside(gain), gate=inside(gate), gain=inside(gain), out=out, residual_out=res)
+        assert torch.equal(bits(out), bits(a[0])) and torch.equal(bits(res), bits(a[1]))
+        for t in bufs:
+            assert (t[:512] == 7).all() and (t[512 + 5 * H:] == 7).all()
+
+
+def test_post_norm_past_32_bits():
+    """Expert rows, tokens and outputs past 4 GiB."""
+    B, H, k = 600000, 4097, 2
+    R = B + 7
+    y = torch.empty(R, H, device="cuda", dtype=torch.bfloat16)
+    for part in y.split(1 << 15):
+        part.normal_(generator=gen(3))
+    r = torch.empty(B, H, device="cuda", dtype=torch.bfloat16)
+    for part in r.split(1 << 15):
+        part.normal_(generator=gen(4))
+    position = torch.stack([torch.arange(B, device="cuda"), R - 1 - torch.arange(B, device="cuda")], 1).int()
+    w, gain = torch.full((B, k), 0.5, device="cuda"), torch.ones(H, device="cuda")
+    out, res, _, _ = md.moe_post_norm(y, r, post_gain=gain, gain=gain, position=position, topk_w=w)
+    for rows in (slice(0, 3), slice(B - 3, B), slice(524200, 524300)):
+        a, b, _, _ = md.moe_post_norm(y[position[rows].long()].flatten(0, 1), r[rows].clone(), post_gain=gain, gain=gain,
+                                      position=torch.arange(2 * (rows.stop - rows.start), device="cuda", dtype=torch.int32).view(-1, 2),
+                                      topk_w=w[rows].clone())
+        n = rows.stop - rows.start
+        assert torch.equal(bits(out[rows]), bits(a)) and torch.equal(bits(res[rows]), bits(b)) and n == a.shape[0]
 
 
 def test_post_norm_in_place():
