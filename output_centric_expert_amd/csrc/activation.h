@@ -1,8 +1,7 @@
-// Activations of the dense product and gates of the norm behind a block, in float32.
-//
-// exp(-x) is the hardware's base-2 exponential of -x log2(e), whose product is taken with its rounding error, so that the
-// error stays at two units in the last place over the whole range (the bare exponential of a rounded product is off by
-// |x| 2^-24); sigmoids are its reciprocal. Arguments below -87 count as -87: the results there are 0 to 1e-36.
+// Activations of the dense product and gates of the norm behind a block, in float32, on the hardware's base-2 exponential
+// and reciprocal (one unit in the last place each; the argument's rounding makes (|v| + 3) 2^-24 of a sigmoid at most).
+// The epilogue of a product is bound by these instructions: five for a SiLU. An exponential past float32's range makes the
+// reciprocal 0.
 #pragma once
 
 #include "block.h"
@@ -11,27 +10,15 @@ namespace moed {
 
 namespace {
 
-// exp(-x) for -88 < x; x up to infinity.
-__device__ __forceinline__ float exp_neg(float x)
-{
-    x = x > 200.0f ? 200.0f : x;
-    const float t = -x * 0x1.715476p+0f;
-    const float low = __builtin_fmaf(-x, 0x1.4ae0bep-26f, __builtin_fmaf(-x, 0x1.715476p+0f, -t));
-    const float e = __builtin_amdgcn_exp2f(t);
-    return __builtin_fmaf(e, low * 0x1.62e43p-1f, e);
-}
-
-__device__ __forceinline__ float at_least_m87(float v) { return v < -87.0f ? -87.0f : v; }      // a NaN stays
-
 __device__ __forceinline__ float sigmoid(float v)
 {
-    return __builtin_amdgcn_rcpf(1.0f + exp_neg(at_least_m87(v)));
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.442695041f * v));
 }
 
 // tanh(v): an odd polynomial (Taylor's) next to zero, where 1 - exp(-2|v|) would lose digits.
 __device__ __forceinline__ float tanh_of(float v)
 {
-    const float a = __builtin_fabsf(v), e = exp_neg(2.0f * a), q = v * v;
+    const float a = __builtin_fabsf(v), e = __builtin_amdgcn_exp2f(-2.885390082f * a), q = v * v;
     float p = __builtin_fmaf(q, 0x1.664f48p-6f, -0x1.ba1ba2p-5f);
     p = __builtin_fmaf(q, p, 0x1.111112p-3f);
     p = __builtin_fmaf(q, p, -0x1.555556p-2f);
@@ -47,18 +34,18 @@ __device__ __forceinline__ void activate(float (&v)[V], int act)
     case kActSilu:
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            v[i] = at_least_m87(v[i]) * sigmoid(v[i]);
+            v[i] = v[i] * sigmoid(v[i]);
         break;
     case kActGelu:                                            // 1 + erf(z) = erfc(-z), without cancellation
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            v[i] = 0.5f * at_least_m87(v[i]) * erfcf(-0.70710678f * at_least_m87(v[i]));
+            v[i] = 0.5f * v[i] * erfcf(-0.70710678f * v[i]);
         break;
     case kActGeluTanh:                                        // (1 + tanh(u)) / 2 = sigmoid(2u)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const float u = 1.5957691f * __builtin_fmaf(0.044715f * v[i] * v[i], v[i], v[i]);
-            v[i] = at_least_m87(v[i]) * sigmoid(u);
+            v[i] = v[i] * sigmoid(u);
         }
         break;
     case kActRelu:

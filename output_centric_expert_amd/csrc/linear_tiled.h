@@ -394,16 +394,24 @@ moe_linear_tiled_kernel(LinearArgs p, LinearPlan plan)
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         bias[i] = p.bias && i < have ? value_at(p.bias_bf16, p.bias, (size_t)n8 + i) : 0.0f;
-    const bool partial = plan.splits > 1;
+    const bool partial = plan.splits > 1, add = p.residual && !partial;
+    const size_t b0 = m0 + (size_t)(wr * RT) * 16;            // this wavefront's first row
+    const int rows = b0 >= (size_t)p.B ? 0 : (size_t)p.B - b0 < (size_t)RT * 16 ? (int)((size_t)p.B - b0) : RT * 16;
+    const int live = have > 0 ? rows : 0;
+    const size_t at0 = b0 * (size_t)p.N + (size_t)n8;
+    // Values of the residual come two turns ahead.
+    constexpr int kTurnsAhead = 2;
+    Raw queue[kTurnsAhead];
+    auto ask = [&](int i, Raw& r) {
+        if (add && i < live)
+            r = have >= 8 ? load_raw<true>(p.residual_bf16, p.residual, at0 + (size_t)i * (size_t)p.N)
+                          : load_short(p.residual_bf16, p.residual, at0 + (size_t)i * (size_t)p.N, have);
+    };
+#pragma unroll
+    for (int q = 0; q < kTurnsAhead; ++q)
+        ask(i8 + q * kRowsAtOnce, queue[q]);
 #pragma unroll
     for (int part = 0; part < RT / S::kStrips; ++part) {
-        const size_t b0 = m0 + (size_t)(wr * RT + part * S::kStrips) * 16;
-        const int rows = b0 >= (size_t)p.B ? 0 : (size_t)p.B - b0 < (size_t)S::kStrips * 16 ? (int)((size_t)p.B - b0) : S::kStrips * 16;
-        const int live = have > 0 ? rows : 0;
-        const size_t at0 = b0 * (size_t)p.N + (size_t)n8;
-        float next[8] = {};                                   // of the residual, asked for one turn ahead
-        if (p.residual && !partial && i8 < live)
-            load_some(p.residual_bf16, p.residual, at0 + (size_t)i8 * (size_t)p.N, have, next);
 #pragma unroll
         for (int r = 0; r < S::kStrips; ++r)
 #pragma unroll
@@ -411,22 +419,27 @@ moe_linear_tiled_kernel(LinearArgs p, LinearPlan plan)
                 *reinterpret_cast<f32x4*>(mine + (r * 16 + col) * S::kOutRow + f * 16 + 4 * g) = acc[part * S::kStrips + r][f];
         wave_lds_fence();
 #pragma unroll 1
-        for (int i = i8; i < live; i += kRowsAtOnce) {
-            const f32x4 lo = *reinterpret_cast<const f32x4*>(mine + i * S::kOutRow + c8);
-            const f32x4 hi = *reinterpret_cast<const f32x4*>(mine + i * S::kOutRow + c8 + 4);
+        for (int at_lds = i8; at_lds < S::kStrips * 16; at_lds += kRowsAtOnce) {
+            const int i = part * S::kStrips * 16 + at_lds;
+            const Raw residual = queue[0];
+#pragma unroll
+            for (int q = 0; q + 1 < kTurnsAhead; ++q)
+                queue[q] = queue[q + 1];
+            ask(i + kTurnsAhead * kRowsAtOnce, queue[kTurnsAhead - 1]);
+            if (i >= live)
+                continue;
+            const f32x4 lo = *reinterpret_cast<const f32x4*>(mine + at_lds * S::kOutRow + c8);
+            const f32x4 hi = *reinterpret_cast<const f32x4*>(mine + at_lds * S::kOutRow + c8 + 4);
             float o[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
             const size_t at = at0 + (size_t)i * (size_t)p.N;
             if (partial) {
                 store_any<false>(plan.partial + (size_t)split * (size_t)p.B * (size_t)p.N, at, have, o);
                 continue;
             }
-            float residual[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-                residual[q] = next[q];
-            if (p.residual && i + kRowsAtOnce < live)
-                load_some(p.residual_bf16, p.residual, at + (size_t)kRowsAtOnce * (size_t)p.N, have, next);
-            linear_finish(p, bias, residual, o);
+            float more[8] = {};
+            if (add)
+                raw_values(p.residual_bf16, residual, more);
+            linear_finish(p, bias, more, o);
             store_some(p.out_bf16, p.out, at, have, o);
         }
         wave_lds_fence();

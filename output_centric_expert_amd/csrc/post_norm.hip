@@ -19,32 +19,6 @@ namespace moed {
 
 namespace {
 
-// Eight values as they lie in memory: bfloat16 (b unused) or float32.
-struct Raw {
-    u32x4 a, b;
-};
-
-template <bool NT>
-__device__ __forceinline__ Raw load_raw(bool bf16, const void* p, size_t at)
-{
-    Raw r;
-    if (bf16) {
-        r.a = ld_at2<NT>(static_cast<const uint16_t*>(p) + at);
-        r.b = u32x4{0, 0, 0, 0};
-    } else {
-        r.a = __builtin_bit_cast(u32x4, ld_at4<NT>(static_cast<const float*>(p) + at));
-        r.b = __builtin_bit_cast(u32x4, ld_at4<NT>(static_cast<const float*>(p) + at + 4));
-    }
-    return r;
-}
-
-__device__ __forceinline__ float raw_value(bool bf16, const Raw& r, int v)
-{
-    if (bf16)
-        return v & 1 ? bf16_hi(r.a[v / 2]) : bf16_lo(r.a[v / 2]);
-    return __uint_as_float(v < 4 ? r.a[v & 3] : r.b[v & 3]);
-}
-
 // Where a thread's piece lies in the row.
 struct Piece {
     int at, skip;
@@ -59,27 +33,10 @@ __device__ __forceinline__ Piece piece_of(int h, int H)
     return {h < last ? h : last, h < last ? 0 : h - last, h < H};
 }
 
-// Rows shorter than a piece go value by value.
-__device__ __forceinline__ Raw load_short(bool bf16, const void* p, size_t at, int H)
-{
-    Raw r = {};
-#pragma unroll
-    for (int v = 0; v < 7; ++v)
-        if (v < H) {
-            if (bf16)
-                r.a[v / 2] |= (uint32_t)static_cast<const uint16_t*>(p)[at + v] << (16 * (v & 1));
-            else if (v < 4)
-                r.a[v & 3] = static_cast<const uint32_t*>(p)[at + v];
-            else
-                r.b[v & 3] = static_cast<const uint32_t*>(p)[at + v];
-        }
-    return r;
-}
-
 template <bool NT>
 __device__ __forceinline__ Raw load_piece(bool bf16, const void* p, size_t row, const Piece& piece, int H)
 {
-    return H < 8 ? load_short(bf16, p, row, H) : load_raw<NT>(bf16, p, row + piece.at);
+    return H < 8 ? load_short(bf16, p, row, H) : load_raw<NT>(bf16, p, row + piece.at);     // rows shorter than a piece
 }
 
 __device__ __forceinline__ void store_piece(bool bf16, void* p, size_t row, const Piece& piece, int H, const float (&v)[8])
@@ -217,10 +174,13 @@ moe_post_norm_kernel(PostNormArgs p)
                         rows[j] = load_piece<true>(YBF16, p.y, (size_t)pos[j0 + j] * (size_t)H, piece[i], H);
 #pragma unroll
                 for (int j = 0; j < kAhead; ++j)
-                    if (j0 + j < p.k)
+                    if (j0 + j < p.k) {
+                        float one[8];
+                        raw_values(YBF16, rows[j], one);
 #pragma unroll
                         for (int v = 0; v < 8; ++v)
-                            s[i][v] = __builtin_fmaf(w[j0 + j], raw_value(YBF16, rows[j], v), s[i][v]);
+                            s[i][v] = __builtin_fmaf(w[j0 + j], one[v], s[i][v]);
+                    }
             }
         }
         if constexpr (kEarly)
@@ -235,10 +195,13 @@ moe_post_norm_kernel(PostNormArgs p)
                 if (piece[i].mine)
                     load_gains(i);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < NV; ++i) {
+            raw_values(YBF16, y[i], s[i]);
+            if (!piece[i].mine)
 #pragma unroll
-            for (int v = 0; v < 8; ++v)
-                s[i][v] = piece[i].mine ? raw_value(YBF16, y[i], v) : 0.0f;
+                for (int v = 0; v < 8; ++v)
+                    s[i][v] = 0.0f;
+        }
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i)                              // values of other pieces
@@ -255,15 +218,20 @@ moe_post_norm_kernel(PostNormArgs p)
             continue;
         if constexpr (!kEarly)
             load_gains(i);
-        if (p.post_gain)
+        if (p.post_gain) {
+            float g[8];
+            raw_values(p.post_gain_bf16, post_gain[i], g);
 #pragma unroll
             for (int v = 0; v < 8; ++v)
-                s[i][v] = s[i][v] * post.mul * post.scale * raw_value(p.post_gain_bf16, post_gain[i], v);
-        float g[8];
+                s[i][v] = s[i][v] * post.mul * post.scale * g[v];
+        }
+        float g[8], held[8];
+        raw_values(RBF16, r[i], held);
 #pragma unroll
         for (int v = 0; v < 8; ++v)
-            g[v] = p.gate_shape >= kGateChannel ? raw_value(p.gate_bf16, gate[i], v) : one_gate;
+            g[v] = one_gate;
         if (p.gate_shape >= kGateChannel) {
+            raw_values(p.gate_bf16, gate[i], g);
             if (p.gate_act != kActNone)
 #pragma unroll
                 for (int v = 0; v < 8; ++v)
@@ -275,7 +243,7 @@ moe_post_norm_kernel(PostNormArgs p)
 #pragma unroll
         for (int v = 0; v < 8; ++v)
             s[i][v] = v < piece[i].skip || (H < 8 && v >= H)
-                ? 0.0f : __builtin_fmaf(p.residual_scale, raw_value(RBF16, r[i], v), g[v] * s[i][v]);
+                ? 0.0f : __builtin_fmaf(p.residual_scale, held[v], g[v] * s[i][v]);
         if (p.residual_out)
             store_piece(RBF16, p.residual_out, row, piece[i], H, s[i]);
     }
@@ -287,9 +255,10 @@ moe_post_norm_kernel(PostNormArgs p)
         if (!piece[i].mine)
             continue;
         float o[8];
+        raw_values(p.gain_bf16, gain[i], o);
 #pragma unroll
         for (int v = 0; v < 8; ++v)
-            o[v] = s[i][v] * pre.mul * pre.scale * raw_value(p.gain_bf16, gain[i], v);
+            o[v] = s[i][v] * pre.mul * pre.scale * o[v];
         if (p.out)
             store_piece(p.out_bf16, p.out, row, piece[i], H, o);
         if (p.q) {                                            // H is a multiple of 32: four whole lanes per block

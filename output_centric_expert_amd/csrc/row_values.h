@@ -159,6 +159,60 @@ __device__ __forceinline__ void store_any(void* p, size_t at, int n, const float
     }
 }
 
+// Eight values as they lie in memory, from any element on: bfloat16 (b unused) or float32. What is loaded well ahead of its
+// use stays raw: a conversion behind a load waits for it.
+struct Raw {
+    u32x4 a, b;
+};
+
+template <bool NT>
+__device__ __forceinline__ Raw load_raw(bool bf16, const void* p, size_t at)
+{
+    Raw r;
+    if (bf16) {
+        r.a = ld_at2<NT>(static_cast<const uint16_t*>(p) + at);
+        r.b = u32x4{0, 0, 0, 0};
+    } else {
+        r.a = __builtin_bit_cast(u32x4, ld_at4<NT>(static_cast<const float*>(p) + at));
+        r.b = __builtin_bit_cast(u32x4, ld_at4<NT>(static_cast<const float*>(p) + at + 4));
+    }
+    return r;
+}
+
+__device__ __forceinline__ void raw_values(bool bf16, const Raw& r, float (&v)[8])
+{
+    if (bf16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = bf16_lo(r.a[i]);
+            v[2 * i + 1] = bf16_hi(r.a[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = __uint_as_float(r.a[i]);
+            v[4 + i] = __uint_as_float(r.b[i]);
+        }
+    }
+}
+
+// Fewer than eight, value by value; zeros behind.
+__device__ __forceinline__ Raw load_short(bool bf16, const void* p, size_t at, int n)
+{
+    Raw r = {};
+#pragma unroll
+    for (int v = 0; v < 7; ++v)
+        if (v < n) {
+            if (bf16)
+                r.a[v / 2] |= (uint32_t)static_cast<const uint16_t*>(p)[at + v] << (16 * (v & 1));
+            else if (v < 4)
+                r.a[v & 3] = static_cast<const uint32_t*>(p)[at + v];
+            else
+                r.b[v & 3] = static_cast<const uint32_t*>(p)[at + v];
+        }
+    return r;
+}
+
 }  // namespace
 
 }  // namespace moed
