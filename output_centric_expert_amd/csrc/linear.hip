@@ -78,7 +78,12 @@ moe_linear_join_kernel(LinearArgs p, const float* partial, int splits, unsigned 
 
 namespace {
 
-constexpr int kSkinnyTiles = 400;                 // tiles up to which a product of more than 16 rows is a skinny one
+// Tiles up to which a product of more than 16 rows is a skinny one: beyond, the chip is full of workgroups that load the same
+// rows. Mixed types, K = 7168: 64 tiles 10.6 us, with the other kernel 12.4; bfloat16, K = 4096: 512 tiles 14.4 and 13.8.
+constexpr int kSkinnyTiles = 400;
+// A wavefront's us a step of the skinny kernel, by the float32 operands and the 16-row fragments of the side with few.
+constexpr float kSkinnyStep[3][2] = {{0.26f, 0.40f}, {0.50f, 0.65f}, {0.40f, 0.55f}};
+constexpr float kSkinnySplitPays = 3.3f;          // us of steps from which a second launch pays
 
 struct Choice {
     enum Kind { dot, skinny, tiled } kind;
@@ -116,11 +121,15 @@ Choice choose(int B, int K, int N, bool x_bf16, bool w_bf16)
         const long long tiles = (long long)s.few_blocks * s.many_blocks;
         if (few <= 16 || tiles <= kSkinnyTiles) {
             c.kind = Choice::skinny;
-            // workgroups for the whole chip, but a step and a half at least for a wavefront
+            // k is split where that saves more than a second launch costs: workgroups for the whole chip then, but a step
+            // and a half at least for a wavefront. 16 rows of bfloat16, 256 outputs: K = 4096 5.3 us whole and 6.7 split,
+            // 5760 7.5 and 7.3, 8192 8.8 and 7.9; 32 rows of float32: K = 1024 6.6 and 7.4, 2048 9.9 and 7.9, 8192 26.7 and 9.7.
+            const int steps = (K + step - 1) / step;
+            const float whole = (float)steps / kSkinnyWaves * kSkinnyStep[(x_bf16 ? 0 : 1) + (w_bf16 ? 0 : 1)][c.rt - 1];
             long long splits = 256 / tiles;
-            const long long most = (K + step - 1) / step * 2 / (3 * kSkinnyWaves);
+            const long long most = (long long)steps * 2 / (3 * kSkinnyWaves);
             splits = splits < most ? splits : most;
-            c.splits = s.splits = (int)(splits < 1 ? 1 : splits);
+            c.splits = s.splits = whole < kSkinnySplitPays || splits < 1 ? 1 : (int)splits;
             return c;
         }
     }
@@ -165,8 +174,8 @@ namespace {
 
 hipError_t launch_join(const LinearArgs& p, const float* partial, int splits, hipStream_t s)
 {
-    // below, single outputs fill the chip sooner
-    if ((size_t)p.B * (size_t)p.N >= 1u << 18) {
+    // 2^20 outputs: 25.3 us with 8 a thread, 26.1 with one (256 x 4096 x 4096 bfloat16); 2^19: 18.2 and 17.9; 2^14: 10.2 and 9.0
+    if ((size_t)p.B * (size_t)p.N >= 1u << 20) {
         const unsigned threads = (unsigned)p.B * (((unsigned)p.N + 7) / 8);
         hipLaunchKernelGGL(moe_linear_join_kernel<8>, dim3((threads + 255) / 256), dim3(256), 0, s, p, partial, splits, threads);
     } else {

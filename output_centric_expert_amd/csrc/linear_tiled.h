@@ -219,7 +219,7 @@ moe_linear_tiled_kernel(LinearArgs p, LinearPlan plan)
         // the step's second half under the first; without the fences the compiler reads them as late as it can (225
         // instead of 214 us). One barrier a step, the first fragments of the next one read under the last turns and all
         // loads issued together behind it, takes 234.
-        static_assert(S::kBK == 64 && RT > NT, "two halves of a step, and turns for the fragments of w");
+        static_assert(S::kBK == 64 && RT >= NT + 2, "two halves of a step; of x at least two reads behind the last of w");
         uint8_t* const wlds = lds + 3 * X::kBytes;
         const int end = st1 < full ? st1 : full;
         auto load_x = [&](int st, int buffer) { x.load(st, lds0 + (uint32_t)(buffer * X::kBytes), w); };

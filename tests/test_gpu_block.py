@@ -76,7 +76,9 @@ SIZES = [(1, 1, 1), (1, 2048, 128), (1, 7168, 256), (2, 33, 5), (3, 1111, 777), 
          (36, 998, 3244), (3225, 1189, 33), (2369, 33, 1717), (133, 2816, 3586), (3943, 2765, 130), (3491, 850, 33),
          (36, 887, 3461), (2299, 35, 1812), (2765, 1296, 641), (808, 1319, 2466), (3427, 884, 33), (34, 971, 3354),
          (4340, 2106, 71), (259, 37, 3333), (35, 604, 3665), (33, 613, 3401), (3271, 40, 37), (34, 1292, 3557), (36, 1325, 3674),
-         (18, 1492, 20), (18, 1561, 19), (19, 1724, 18), (19, 1963, 18), (20, 890, 18), (21, 789, 18)]
+         (18, 1492, 20), (18, 1561, 19), (19, 1724, 18), (19, 1963, 18), (20, 890, 18), (21, 789, 18),
+         # the same of the kernel of few rows
+         (5, 9001, 40), (2000, 9001, 7), (400, 9004, 16), (40, 5001, 24), (24, 5003, 100), (6, 8194, 40)]
 
 
 @pytest.mark.parametrize("B,K,N", SIZES)
