@@ -569,7 +569,8 @@ typedef enum {
  *              are not used)
  *   post_gain  [H] post_gain_dtype, or NULL
  *   gate       a moed_gate shape of gate_dtype; NULL with MOED_GATE_NONE
- *   gate_act   MOED_ACT_NONE, MOED_ACT_SIGMOID or MOED_ACT_TANH
+ *   gate_act   MOED_ACT_NONE, MOED_ACT_SIGMOID or MOED_ACT_TANH; of no effect
+ *              without a gate
  *   residual   [B][H] residual_dtype
  *   residual_out  [B][H] residual_dtype, or NULL: not stored; may be the residual,
  *              or y [B][H] where the types agree

@@ -696,7 +696,7 @@ def moe_post_norm(y, residual, post_gain=None, post_eps: float = 1e-6, gate=None
     are out's values in MXFP8, else None.
     y is [B, H]; with position int32 [B, k] and topk_w float32 [B, k] it is the experts' rows [R, H], and their weighted
     sum (moe_combine's) is taken. gate: one number a token [B, 1], a channel [H] or [1, H], or each [B, H]; gate_act:
-    None, "sigmoid" or "tanh". Give the residual as residual_out for an update in place."""
+    None, "sigmoid" or "tanh", of no effect without a gate. Give the residual as residual_out for an update in place."""
     dev = _current_device()
     if y.dim() != 2 or residual.dim() != 2:
         raise ValueError("expected y [B, H] (or [R, H] with position) and residual [B, H]")
@@ -719,8 +719,6 @@ def moe_post_norm(y, residual, post_gain=None, post_eps: float = 1e-6, gate=None
         gs = tuple(gate.shape) if isinstance(gate, torch.Tensor) else None
         kind = 3 if gs == (B, H) else 2 if gs == (H,) or gs == (1, H) else 1
         gp, gd = _operand(gate, "gate", gs if kind > 1 else (B, 1), dev)
-    elif act:
-        raise ValueError("gate_act needs a gate")
     else:
         gp, gd, kind = None, 0, 0
     if quantize and H % 32:

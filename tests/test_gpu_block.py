@@ -611,12 +611,22 @@ def test_post_norm_special_values():
     assert torch.equal(res, tiny) and ((out.double() - ref).abs() <= 70 * U * ref.abs()).all()
 
 
+@pytest.mark.parametrize("act", ["sigmoid", "tanh"])
+def test_post_norm_without_a_gate(act):
+    """An activation of no gate has no effect."""
+    g = gen(23)
+    y, r, gain = randn(g, 5, 320), randn(g, 5, 320), randn(g, 320)
+    for a, b in zip(md.moe_post_norm(y, r, gain=gain, scale=0.7, quantize=True),
+                    md.moe_post_norm(y, r, gain=gain, scale=0.7, quantize=True, gate_act=act)):
+        assert torch.equal(bits(a), bits(b))
+
+
 def test_post_norm_empty_and_refusals():
     y, r, gain = torch.ones(4, 64, device="cuda"), torch.ones(4, 64, device="cuda"), torch.ones(64, device="cuda")
     assert md.moe_post_norm(y[:0], r[:0], gain=gain)[0].shape == (0, 64)
     pos, w = torch.zeros(4, 2, dtype=torch.int32, device="cuda"), torch.ones(4, 2, device="cuda")
     for kw, err in (({"out": y}, ValueError), ({"quantize": True}, ValueError), ({"gain": gain, "out_dtype": None}, ValueError),
-                    ({"gate_act": "tanh"}, ValueError), ({"gate": gain, "gate_act": "silu"}, ValueError), ({"gate": w}, ValueError),
+                    ({"gate_act": "silu"}, ValueError), ({"gate": gain, "gate_act": "silu"}, ValueError), ({"gate": w}, ValueError),
                     ({"position": pos}, ValueError), ({"topk_w": w}, ValueError), ({"position": pos[:3], "topk_w": w[:3]}, ValueError),
                     ({"gain": gain, "out_q": y}, ValueError), ({"post_gain": gain[:32]}, ValueError), ({"gain": gain.half()}, TypeError),
                     ({"gain": gain, "out": r, "residual_out": r}, md.MoedError), ({"post_eps": -1.0}, md.MoedError)):
