@@ -205,10 +205,12 @@ hipError_t launch_linear(const LinearArgs& p, bool x_bf16, bool w_bf16, void* wo
     c.plan.partial = c.skinny_plan.partial = static_cast<float*>(workspace);
     hipError_t e;
     if (c.kind == Choice::skinny) {
-        auto launch = x_bf16 ? (w_bf16 ? launch_skinny_bf16 : launch_skinny_mixed_w) : (w_bf16 ? launch_skinny_mixed_x : launch_skinny_f32);
+        auto launch = x_bf16 ? (w_bf16 ? launch_skinny_bf16 : launch_skinny_mixed_w)
+                             : (w_bf16 ? launch_skinny_mixed_x : launch_skinny_f32);
         e = launch(c.swapped, c.rt, p, c.skinny_plan, s);
     } else {
-        auto launch = x_bf16 ? (w_bf16 ? launch_linear_bf16 : launch_linear_mixed_w) : (w_bf16 ? launch_linear_mixed_x : launch_linear_f32);
+        auto launch = x_bf16 ? (w_bf16 ? launch_linear_bf16 : launch_linear_mixed_w)
+                             : (w_bf16 ? launch_linear_mixed_x : launch_linear_f32);
         e = launch(c.tile, p, c.plan, s);
     }
     if (e != hipSuccess || c.splits == 1)

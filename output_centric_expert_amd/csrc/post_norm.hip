@@ -8,7 +8,9 @@
 // A row stays in the registers of its threads (8 values a piece, NV pieces a thread, TPR threads a row) from the loads to
 // the last store; two sums over the row stand between them. All loads are asked for in front of the first use of any
 // (raw: a conversion behind a load waits for it), so that a row waits for memory once, twice where its rows' places
-// come first. Memory bound.
+// come first. Memory bound: 8192 tokens of 4096 values, bfloat16, with MXFP8 55-57 us (5.4 TB/s), 8 expert rows a token of
+// 2048 and a float32 residual 76 us (5.7 TB/s; 105 with conversions between the loads), rows of 1111 values 24 us (3 TB/s:
+// their pieces begin at any element, and their stores do not fill lines); one token 3-4 us, two round trips and the launch.
 // Rows may begin at any element and have any length: a piece that would pass the row's end is the row's last 8 values
 // instead, of which the first `skip` are another piece's: loaded, but neither counted nor stored.
 #include "activation.h"
