@@ -493,8 +493,8 @@ typedef enum {
  * workspace: at least moe_linear_workspace_bytes(...) bytes (0 for invalid
  * arguments), 16-byte aligned; NULL where that is 0.
  * Limits (MOED_ERR_SHAPE): 1 <= K, N < 2^20; K*N below 2^32; B*K below 2^40,
- * B*N below 2^38. x, w, residual and out are 16-byte aligned, bias by its element
- * (MOED_ERR_ALIGN). B = 0 launches nothing.
+ * B*N below 2^38; out is not x, w or the workspace. x, w, residual and out are
+ * 16-byte aligned, bias by its element (MOED_ERR_ALIGN). B = 0 launches nothing.
  */
 size_t moe_linear_workspace_bytes(int B, int K, int N, int x_dtype, int w_dtype);
 int moe_linear(const void *x, int x_dtype, const void *w, int w_dtype,
@@ -580,8 +580,8 @@ typedef enum {
  *              types agree
  *   out_q, out_s  [B][H] codes and [B][H/32] scales, or both NULL
  * One of residual_out, out and out_q must be given. Outputs overlap nothing
- * else; out and residual_out are not the same (MOED_ERR_SHAPE). Squares as in
- * moe_norm().
+ * else; out and residual_out are not the same, and with a position neither is y
+ * (MOED_ERR_SHAPE). Squares as in moe_norm().
  * Limits (MOED_ERR_SHAPE): 1 <= H <= 32768, a multiple of 32 with out_q;
  * eps, post_eps >= 0; with a position 1 <= k <= 64 and 0 <= R < 2^28. Pointers of
  * y, post_gain, residual, residual_out, gain, out and out_q are 16-byte aligned,

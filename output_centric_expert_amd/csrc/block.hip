@@ -60,6 +60,8 @@ int moe_linear(const void* x, int x_dtype, const void* w, int w_dtype, const voi
     if (!aligned16(x) || !aligned16(w) || !aligned16(residual) || !aligned16(out) || (need && !aligned16(workspace)) ||
         (bias && !aligned(bias, bias_dtype == MOED_BF16 ? 2 : 4)))
         return MOED_ERR_ALIGN;
+    if (out == x || out == w || (need && (out == workspace || residual == workspace)))   // read after outputs are written
+        return MOED_ERR_SHAPE;
     moed::LinearArgs p;
     p.x = x; p.w = w; p.bias = bias; p.residual = residual; p.out = out;
     p.B = B; p.K = K; p.N = N; p.act = activation;
@@ -129,6 +131,8 @@ int moe_post_norm(const void* y, int y_dtype, int R, const int32_t* position, co
         !aligned16(gain) || !aligned16(out) || !aligned16(out_q) || !aligned(position, 4) || !aligned(topk_w, 4))
         return MOED_ERR_ALIGN;
     if (out && out == residual_out)                           // the sum would be lost
+        return MOED_ERR_SHAPE;
+    if (position && y && (y == residual_out || y == out))     // other tokens read those rows
         return MOED_ERR_SHAPE;
     moed::PostNormArgs p;
     p.y = y; p.position = position; p.topk_w = topk_w; p.post_gain = post_gain; p.gate = gate; p.residual = residual;

@@ -79,3 +79,15 @@ def test_post_norm_rejects(lib):  # noqa: F811
     assert post(lib, g=MIS, gs=2) == md.MOED_ERR_ALIGN
     same = A.value + 4096 if hasattr(A, "value") else A + 4096
     assert post(lib, ro=same, out=A) == md.MOED_ERR_SHAPE
+    # the experts' rows are not overwritten
+    assert post(lib, pos=A, tw=A, ro=A) == md.MOED_ERR_SHAPE
+    assert post(lib, pos=A, tw=A, ro=None, y=same) == md.MOED_ERR_SHAPE
+
+
+def test_linear_outputs_overlap_nothing(lib):  # noqa: F811
+    at = getattr(A, "value", A)
+    need = lib.moe_linear_workspace_bytes(64, 7168, 256, 0, 0)
+    assert need > 0
+    for kw in ({"out": at}, {"x": at + 4096, "out": at + 4096, "ws": at + 8192}, {"w": at + 4096, "out": at + 4096, "ws": at + 8192},
+               {"out": at + 4096, "ws": at + 4096}, {"out": at + 4096, "r": at + 8192, "ws": at + 8192}):
+        assert linear(lib, B=64, K=7168, N=256, wsb=need, **kw) == md.MOED_ERR_SHAPE, kw
