@@ -732,6 +732,35 @@ def test_captured_and_replayed(B, prefill):
         md.moe_linear(randn(gen(seed), 64, 7168).bfloat16(), randn(gen(9), 256, 7168))
 
 
+def test_captured_with_one_workspace():
+    """Two graphs whose products are split and whose sums lie in the same workspace, replayed in turn."""
+    types = (torch.bfloat16, torch.float32)
+    sizes = [(64, 7168, 256), (700, 4096, 900)]
+    need = [md.moe_linear_workspace_bytes(*size, *types) for size in sizes]
+    assert min(need) > 0
+    ws = torch.empty(max(need), dtype=torch.uint8, device="cuda")
+    calls = []
+    for i, (B, K, N) in enumerate(sizes):
+        g = gen(60 + i)
+        calls.append([randn(g, B, K).bfloat16(), randn(g, N, K), randn(g, B, N), torch.empty(B, N, device="cuda")])
+    graphs = []
+    for x, w, r, out in calls:
+        md.moe_linear(x, w, residual=r, activation="tanh", out=out, workspace=ws)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            md.moe_linear(x, w, residual=r, activation="tanh", out=out, workspace=ws)
+    for rep in range(3):
+        for i, (x, w, r, out) in enumerate(calls):
+            x.copy_(randn(gen(70 + 2 * rep + i), *x.shape))
+            out.fill_(float("nan"))
+        for g in graphs + graphs[::-1]:
+            g.replay()
+        torch.cuda.synchronize()
+        for x, w, r, out in calls:
+            assert torch.equal(bits(out), bits(md.moe_linear(x, w, residual=r, activation="tanh", out_dtype=torch.float32)))
+
+
 def test_two_streams():
     """Calls on streams of their own, handed over as stream or as a raw handle; results made by the call."""
     halves = [Half(64, seed=7), Half(64, seed=8)]
