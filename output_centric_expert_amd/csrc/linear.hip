@@ -81,9 +81,9 @@ namespace {
 // Tiles up to which a product of more than 16 rows is a skinny one: beyond, the chip is full of workgroups that load the same
 // rows. Mixed types, K = 7168: 64 tiles 10.6 us, with the other kernel 12.4; bfloat16, K = 4096: 512 tiles 14.4 and 13.8.
 constexpr int kSkinnyTiles = 400;
-// A wavefront's us a step of the skinny kernel, by the float32 operands and the 16-row fragments of the side with few.
-constexpr float kSkinnyStep[3][2] = {{0.26f, 0.40f}, {0.50f, 0.65f}, {0.40f, 0.55f}};
-constexpr float kSkinnySplitPays = 3.3f;          // us of steps from which a second launch pays
+// A wavefront's us a step of the skinny kernel, by the number of float32 operands (two: steps of 32 values, else of 64).
+constexpr float kSkinnyStep[3] = {0.26f, 0.50f, 0.40f};
+constexpr float kSkinnySplitPays = 4.5f;          // us of steps from which a second launch pays
 
 struct Choice {
     enum Kind { dot, skinny, tiled } kind;
@@ -114,18 +114,21 @@ Choice choose(int B, int K, int N, bool x_bf16, bool w_bf16)
     {
         c.swapped = N < B;
         const int few = c.swapped ? N : B, many = c.swapped ? B : N;
-        c.rt = few <= 16 ? 1 : 2;
+        // 16 x 16 outputs a workgroup where each has a CU of its own then: 32 x 1024 -> 1024 float32 6.2 us (32 x 16: 7.5),
+        // 64 x 4096 -> 1024 bfloat16 6.8 (8.1). Beyond, 32 x 16, which read the side with many half as often.
+        c.rt = few <= 16 || (long long)((few + 15) / 16) * ((many + 15) / 16) <= 256 ? 1 : 2;
         SkinnyPlan& s = c.skinny_plan;
         s.few_blocks = (few + 16 * c.rt - 1) / (16 * c.rt);
         s.many_blocks = (many + 15) / 16;
         const long long tiles = (long long)s.few_blocks * s.many_blocks;
         if (few <= 16 || tiles <= kSkinnyTiles) {
             c.kind = Choice::skinny;
-            // k is split where that saves more than a second launch costs: workgroups for the whole chip then, but a step
-            // and a half at least for a wavefront. 16 rows of bfloat16, 256 outputs: K = 4096 5.3 us whole and 6.7 split,
-            // 5760 7.5 and 7.3, 8192 8.8 and 7.9; 32 rows of float32: K = 1024 6.6 and 7.4, 2048 9.9 and 7.9, 8192 26.7 and 9.7.
+            // k is split where that saves more than a second launch costs, which the host feels more than the GPU: workgroups
+            // for the whole chip then, but a step and a half at least for a wavefront. 16 rows, 256 outputs, bfloat16:
+            // K = 4096 5.3 us whole and 6.7 split, 7168 8.5 and 7.7, 8192 8.8 and 7.9; 64 rows, float32 w: K = 4096 8.7 and
+            // 8.1, 7168 12.0 and 9.5; float32: K = 2048 7.2 and 7.1, 7168 17.6 and 10.7.
             const int steps = (K + step - 1) / step;
-            const float whole = (float)steps / kSkinnyWaves * kSkinnyStep[(x_bf16 ? 0 : 1) + (w_bf16 ? 0 : 1)][c.rt - 1];
+            const float whole = (float)steps / kSkinnyWaves * kSkinnyStep[(x_bf16 ? 0 : 1) + (w_bf16 ? 0 : 1)];
             long long splits = 256 / tiles;
             const long long most = (long long)steps * 2 / (3 * kSkinnyWaves);
             splits = splits < most ? splits : most;

@@ -10,7 +10,7 @@
 //                                          here    the tiles' kernel
 //   32 x 4096 -> 4096 bfloat16             10.6 us   13.3             (3.2 TB/s)
 //   16 x 2048 -> 512 bfloat16               4.4       8.4
-//   64 x 7168 -> 256, w float32             9.1      13.3             (both with k split and a second launch)
+//   64 x 7168 -> 256, w float32             9.5      13.3             (both with k split and a second launch)
 //   8192 x 4096 -> 16 bfloat16             18.9      19.9             (3.6 TB/s)
 // There a barrier a step lets the wavefronts wait together; here others' loads fill in for one's wait.
 #pragma once

@@ -86,8 +86,8 @@ def test_post_norm_rejects(lib):  # noqa: F811
 
 def test_linear_outputs_overlap_nothing(lib):  # noqa: F811
     at = getattr(A, "value", A)
-    need = lib.moe_linear_workspace_bytes(64, 7168, 256, 0, 0)
+    need = lib.moe_linear_workspace_bytes(64, 7168, 256, 1, 1)
     assert need > 0
     for kw in ({"out": at}, {"x": at + 4096, "out": at + 4096, "ws": at + 8192}, {"w": at + 4096, "out": at + 4096, "ws": at + 8192},
                {"out": at + 4096, "ws": at + 4096}, {"out": at + 4096, "r": at + 8192, "ws": at + 8192}):
-        assert linear(lib, B=64, K=7168, N=256, wsb=need, **kw) == md.MOED_ERR_SHAPE, kw
+        assert linear(lib, B=64, K=7168, N=256, xd=1, wd=1, wsb=need, **kw) == md.MOED_ERR_SHAPE, kw

@@ -78,7 +78,7 @@ SIZES = [(1, 1, 1), (1, 2048, 128), (1, 7168, 256), (2, 33, 5), (3, 1111, 777), 
          (4340, 2106, 71), (259, 37, 3333), (35, 604, 3665), (33, 613, 3401), (3271, 40, 37), (34, 1292, 3557), (36, 1325, 3674),
          (18, 1492, 20), (18, 1561, 19), (19, 1724, 18), (19, 1963, 18), (20, 890, 18), (21, 789, 18),
          # the same of the kernel of few rows
-         (5, 9001, 40), (2000, 9001, 7), (400, 9004, 16), (40, 5001, 24), (24, 5003, 100), (6, 8194, 40)]
+         (5, 9001, 40), (2000, 9001, 7), (400, 9004, 16), (40, 5001, 24), (24, 5003, 100), (6, 9002, 40), (3000, 200, 20), (3001, 201, 30)]
 
 
 @pytest.mark.parametrize("B,K,N", SIZES)
