@@ -10,8 +10,8 @@
 // What bounds it, with the chip full: the matrix instructions and the loads' way into LDS, which do not overlap all the time
 // (the matrix unit is busy for half of it). A step of a 256 x 256 bfloat16 tile is 64 KiB in and 8.4 MFLOP. Measured:
 //   bfloat16 x bfloat16  8192 x 8192 x 8192 794 us (1.38 PFLOP/s); 8192 x 4096 x 4096 220 us, with bias, SiLU and residual 234
-//   bfloat16 x float32   8192 x 4096 x 4096 617 us (1.34 PFLOP/s of the three products)
-//   float32 x float32    4096 x 4096 x 4096 597 us (1.38 PFLOP/s of the six)
+//   bfloat16 x float32   8192 x 4096 x 4096 622 us (1.33 PFLOP/s of the three products)
+//   float32 x float32    4096 x 4096 x 4096 582-596 us (1.38-1.42 PFLOP/s of the six)
 // Smaller products are bound by what a step takes on a CU with little of its own work: the trip to LDS and the barrier.
 #pragma once
 
@@ -358,6 +358,12 @@ moe_linear_tiled_kernel(LinearArgs p, LinearPlan plan)
             }
         };
         constexpr int kFetches = X::kFetches + W::kFetches;
+        // Large tiles: half of the wavefronts split their values in front of the products and the others behind them, so that
+        // a SIMD's two use the vector and the matrix unit at the same time (4096 x 4096 x 4096 float32 596 instead of 610-639
+        // us, w alone float32 327 instead of 335). In shorter steps the values are not there that early (1024 x 1024 x 1024
+        // float32 23.8 instead of 22.0), and x alone is no gain (341 and 338).
+        constexpr bool kApart = WF32 && RT * NT >= 16;
+        const bool early = w >= S::kWaves / 2;
         auto step = [&](int st, auto odd) {
             constexpr int kSet = decltype(odd)::value;        // (st - st0) % 2: its buffer, and the registers of st + 2
             // what goes straight to LDS was asked for in front of the fetch of st + 2
@@ -368,14 +374,31 @@ moe_linear_tiled_kernel(LinearArgs p, LinearPlan plan)
                     wait_loads<0>();
             }
             __syncthreads();                                  // step st is in LDS, and nobody reads the one before
-            if (st + 1 < st1)
-                load_or_put(st + 1, kSet ^ 1);
-            compute(kSet, 0);
-            put(kSet ^ 1, kSet ^ 1);                          // behind the last step: something old, which nobody reads
-            if (st + 3 < st1)
-                fetch(kSet ^ 1, st + 3);
-            if constexpr (S::kBK > 32)
-                compute(kSet, 1);
+            auto next = [&] {
+                put(kSet ^ 1, kSet ^ 1);                      // behind the last step: something old, which nobody reads
+                if (st + 3 < st1)
+                    fetch(kSet ^ 1, st + 3);
+            };
+            if constexpr (kApart) {
+                if (early)
+                    put(kSet ^ 1, kSet ^ 1);
+                if (st + 1 < st1)
+                    load_or_put(st + 1, kSet ^ 1);
+                if (early && st + 3 < st1)
+                    fetch(kSet ^ 1, st + 3);
+                compute(kSet, 0);
+                if constexpr (S::kBK > 32)
+                    compute(kSet, 1);
+                if (!early)
+                    next();
+            } else {
+                if (st + 1 < st1)
+                    load_or_put(st + 1, kSet ^ 1);
+                compute(kSet, 0);
+                next();
+                if constexpr (S::kBK > 32)
+                    compute(kSet, 1);
+            }
         };
         load_or_put(st0, 0);
         fetch(0, st0);
