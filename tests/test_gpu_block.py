@@ -145,6 +145,17 @@ def test_linear_in_place_and_neighbours(B, w_type):
     assert torch.equal(buf[:8], before[:8]) and torch.equal(buf[B + 8:], before[B + 8:])
 
 
+@pytest.mark.parametrize("B,K,N", [(1, 64, 77), (40, 9000, 77), (300, 64, 500), (2052, 2877, 904)])
+@pytest.mark.parametrize("bias_type", ["bf16", "f32"])
+def test_linear_bias_at_any_element(B, K, N, bias_type):
+    g = gen(B + N)
+    x, w, b = randn(g, B, K), randn(g, N, K) / math.sqrt(K), randn(g, N + 9).to(TYPES[bias_type])
+    for at in (1, 3, 8):
+        part = b[at:at + N]
+        assert torch.equal(bits(md.moe_linear(x, w, bias=part, out_dtype=torch.float32)),
+                           bits(md.moe_linear(x, w, bias=part.clone(), out_dtype=torch.float32)))
+
+
 @pytest.mark.parametrize("B", [1, 8, 40, 300])
 @pytest.mark.parametrize("x_type,w_type", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
 def test_linear_special_values(B, x_type, w_type):
