@@ -480,7 +480,7 @@ typedef enum {
  *   bias      [N] bias_dtype, or NULL: 0
  *   residual  [B][N] residual_dtype, or NULL: 0; may be out where the types
  *             agree
- *   out       [B][N] out_dtype, rounded once; overlaps nothing else
+ *   out       [B][N] out_dtype, rounded once
  *   activation  a moed_activation
  * K and N are any positive numbers (router logits: N experts; a shared
  * expert's gate: N = 1). Sums are float32 of exact products; float32 operands
@@ -493,8 +493,10 @@ typedef enum {
  * workspace: at least moe_linear_workspace_bytes(...) bytes (0 for invalid
  * arguments), 16-byte aligned; NULL where that is 0.
  * Limits (MOED_ERR_SHAPE): 1 <= K, N < 2^20; K*N below 2^32; B*K below 2^40,
- * B*N below 2^38; out is not x, w or the workspace. x, w, residual and out are
- * 16-byte aligned, bias by its element (MOED_ERR_ALIGN). B = 0 launches nothing.
+ * B*N below 2^38; out and the used part of the workspace share no byte with an
+ * operand or each other, but for a residual of out's type at out's address.
+ * x, w, residual and out are 16-byte aligned, bias by its element
+ * (MOED_ERR_ALIGN). B = 0 launches nothing.
  */
 size_t moe_linear_workspace_bytes(int B, int K, int N, int x_dtype, int w_dtype);
 int moe_linear(const void *x, int x_dtype, const void *w, int w_dtype,

@@ -10,6 +10,22 @@ inline bool aligned(const void* p, unsigned n) { return ((uintptr_t)p & (n - 1))
 inline bool aligned16(const void* p) { return aligned(p, 16); }
 inline bool dtype_ok(int d) { return d == MOED_BF16 || d == MOED_F32; }
 
+// A buffer of `count` elements of a dtype, or of bytes.
+struct Range {
+    const void* p;
+    unsigned long long bytes;
+    int dtype;
+};
+inline Range range(const void* p, int dtype, unsigned long long count) { return {p, count * (dtype == MOED_BF16 ? 2 : 4), dtype}; }
+inline Range bytes(const void* p, unsigned long long count) { return {p, count, -1}; }
+inline bool overlap(const Range& a, const Range& b)
+{
+    const uintptr_t s = (uintptr_t)a.p, t = (uintptr_t)b.p;
+    return s && t && s < t + b.bytes && t < s + a.bytes;
+}
+// out over an operand that is read once, by the thread that writes the same element: one buffer of one type.
+inline bool in_place(const Range& out, const Range& in) { return out.p == in.p && out.dtype == in.dtype; }
+
 static_assert(moed::kActNone == MOED_ACT_NONE && moed::kActSilu == MOED_ACT_SILU && moed::kActGelu == MOED_ACT_GELU &&
                   moed::kActGeluTanh == MOED_ACT_GELU_TANH && moed::kActRelu == MOED_ACT_RELU &&
                   moed::kActSigmoid == MOED_ACT_SIGMOID && moed::kActTanh == MOED_ACT_TANH,
@@ -60,7 +76,15 @@ int moe_linear(const void* x, int x_dtype, const void* w, int w_dtype, const voi
     if (!aligned16(x) || !aligned16(w) || !aligned16(residual) || !aligned16(out) || (need && !aligned16(workspace)) ||
         (bias && !aligned(bias, bias_dtype == MOED_BF16 ? 2 : 4)))
         return MOED_ERR_ALIGN;
-    if (out == x || out == w || (need && (out == workspace || residual == workspace)))   // read after outputs are written
+    const unsigned long long rows = (unsigned long long)B, outputs = rows * (unsigned)N;
+    const Range o = range(out, out_dtype, outputs), r = range(residual, residual_dtype, outputs);
+    const Range ws = bytes(need ? workspace : nullptr, need);
+    const Range in[] = {range(x, x_dtype, rows * (unsigned)K), range(w, w_dtype, (unsigned long long)N * (unsigned)K),
+                        range(bias, bias_dtype, (unsigned)N)};
+    for (const Range& i : in)                                 // read after the first outputs and sums are written
+        if (overlap(o, i) || overlap(ws, i))
+            return MOED_ERR_SHAPE;
+    if ((overlap(o, r) && !in_place(o, r)) || overlap(ws, r) || overlap(ws, o))
         return MOED_ERR_SHAPE;
     moed::LinearArgs p;
     p.x = x; p.w = w; p.bias = bias; p.residual = residual; p.out = out;
