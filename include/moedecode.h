@@ -581,9 +581,9 @@ typedef enum {
  *   out        [B][H] out_dtype, or NULL; may be y [B][H] or the residual where the
  *              types agree
  *   out_q, out_s  [B][H] codes and [B][H/32] scales, or both NULL
- * One of residual_out, out and out_q must be given. Outputs overlap nothing
- * else; out and residual_out are not the same, and with a position neither is y
- * (MOED_ERR_SHAPE). Squares as in moe_norm().
+ * One of residual_out, out and out_q must be given. Outputs share no byte with
+ * anything else, but in place as above: at one address and of one type, and
+ * with a position not with y (MOED_ERR_SHAPE). Squares as in moe_norm().
  * Limits (MOED_ERR_SHAPE): 1 <= H <= 32768, a multiple of 32 with out_q;
  * eps, post_eps >= 0; with a position 1 <= k <= 64 and 0 <= R < 2^28. Pointers of
  * y, post_gain, residual, residual_out, gain, out and out_q are 16-byte aligned,

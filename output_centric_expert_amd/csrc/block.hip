@@ -154,10 +154,24 @@ int moe_post_norm(const void* y, int y_dtype, int R, const int32_t* position, co
     if (!aligned16(y) || !aligned16(post_gain) || !aligned16(gate) || !aligned16(residual) || !aligned16(residual_out) ||
         !aligned16(gain) || !aligned16(out) || !aligned16(out_q) || !aligned(position, 4) || !aligned(topk_w, 4))
         return MOED_ERR_ALIGN;
-    if (out && out == residual_out)                           // the sum would be lost
-        return MOED_ERR_SHAPE;
-    if (position && y && (y == residual_out || y == out))     // other tokens read those rows
-        return MOED_ERR_SHAPE;
+    const unsigned long long rows = (unsigned long long)B, n = rows * (unsigned)H, h = (unsigned)H;
+    const unsigned long long slots = position ? rows * (unsigned)k : 0;
+    const unsigned long long gates = gate_shape == MOED_GATE_TOKEN ? rows : gate_shape == MOED_GATE_CHANNEL ? h : n;
+    const Range outs[] = {range(residual_out, residual_dtype, n), range(out, out_dtype, n), bytes(out_q, n), bytes(out_s, n / 32)};
+    const Range in[] = {range(y, y_dtype, position ? (unsigned)R * h : n), range(residual, residual_dtype, n),
+                        range(gate, gate_dtype, gates), range(post_gain, post_gain_dtype, h), range(gain, gain_dtype, h),
+                        bytes(position, slots * 4), bytes(topk_w, slots * 4)};
+    for (int i = 0; i < 4; ++i) {
+        for (int j = i + 1; j < 4; ++j)
+            if (overlap(outs[i], outs[j]))
+                return MOED_ERR_SHAPE;
+        for (int j = 0; j < 7; ++j) {
+            // with a position other tokens read the rows of y
+            const bool may = i < 2 && (j == 1 || (j == 0 && !position)) && in_place(outs[i], in[j]);
+            if (overlap(outs[i], in[j]) && !may)
+                return MOED_ERR_SHAPE;
+        }
+    }
     moed::PostNormArgs p;
     p.y = y; p.position = position; p.topk_w = topk_w; p.post_gain = post_gain; p.gate = gate; p.residual = residual;
     p.residual_out = residual_out; p.gain = gain; p.out = out; p.q = out_q; p.q_s = out_s;
