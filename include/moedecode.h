@@ -539,8 +539,9 @@ typedef enum {
  * token) and a NaN weight, and the sum is of the others.
  * Limits (MOED_ERR_SHAPE): E <= 2048, 1 <= n_group <= 64, a divisor of E;
  * 1 <= topk_group <= n_group; 1 <= k <= 64 and at most topk_group * E / n_group;
- * n_shared >= 0; B*E and B*(k + n_shared) below 2^31. Unknown logits_dtype,
- * score or group_score: MOED_ERR_DTYPE. B = 0 launches nothing.
+ * n_shared >= 0; B*E and B*(k + n_shared) below 2^31; topk_ids and topk_w share
+ * no byte with the inputs or each other. Unknown logits_dtype, score or
+ * group_score: MOED_ERR_DTYPE. B = 0 launches nothing.
  */
 int moe_route_scored(const void *logits, int logits_dtype, const float *bias, int score,
                      int n_group, int topk_group, int group_score, int renormalize,

@@ -116,6 +116,14 @@ int moe_route_scored(const void* logits, int logits_dtype, const float* bias, in
         return MOED_ERR_NULL;
     if (!aligned(logits, logits_dtype == MOED_BF16 ? 2 : 4) || !aligned(bias, 4) || !aligned(topk_ids, 4) || !aligned(topk_w, 4))
         return MOED_ERR_ALIGN;
+    const unsigned long long rows = (unsigned long long)B, slots = rows * ((unsigned long long)k + (unsigned)n_shared);
+    const Range ids = bytes(topk_ids, slots * 4), w = bytes(topk_w, slots * 4);
+    const Range in[] = {range(logits, logits_dtype, rows * (unsigned)E), bytes(bias, (unsigned long long)E * 4)};
+    for (const Range& i : in)                                 // other tokens read them
+        if (overlap(ids, i) || overlap(w, i))
+            return MOED_ERR_SHAPE;
+    if (overlap(ids, w))
+        return MOED_ERR_SHAPE;
     moed::RouteArgs p;
     p.logits = logits; p.bias = bias; p.ids = topk_ids; p.w = topk_w;
     p.B = B; p.E = E; p.k = k; p.n_shared = n_shared;

@@ -136,3 +136,16 @@ def test_post_norm_outputs_overlap_no_gate(lib, shape, size):  # noqa: F811
     last = (c.places["gate"] + size * 2 - 1) & ~0xF
     for out in POST_OUT:
         assert c.call(gate_shape=shape, **{out: last}) == md.MOED_ERR_SHAPE, out
+
+
+@pytest.mark.parametrize("logits", [BF16, F32])
+@pytest.mark.parametrize("out,name", [("ids", "logits"), ("ids", "bias"), ("ids", "w"), ("w", "logits"), ("w", "bias")])
+def test_route_scored_outputs_overlap_nothing(lib, logits, out, name):  # noqa: F811
+    B, E, k, shared_slots = 100, 64, 8, 1
+    slots = B * (k + shared_slots) * 4
+    sizes = {"logits": B * E * SIZE[logits], "bias": E * 4, "ids": slots, "w": slots}
+    places = place(sizes)
+    for at in shared(places, sizes, out, name):
+        p = {**places, out: at}
+        assert lib.moe_route_scored(P(p["logits"]), logits, P(p["bias"]), 1, 1, 1, 0, 1, B, E, k, shared_slots, 1.0, P(p["ids"]),
+                                    P(p["w"]), None) == md.MOED_ERR_SHAPE, hex(at)
