@@ -267,6 +267,20 @@ int moed_selftest_decode(const uint8_t *codes, const uint8_t *scales, float *out
                          int n, int path, void *stream);
 
 /*
+ * Which kernel moe_linear() takes for a size and two types (moed_dtype), so that
+ * tests can see that each is run. Six numbers to path, in host memory:
+ *   path[0]  0: the kernel of a single row; 1: of few rows; 2: of tiles
+ *   path[1]  few rows: 16-row blocks of the side with few in a workgroup (1 or
+ *            2); tiles: the number of the tile's shape
+ *   path[2]  few rows: 1 where that side is w
+ *   path[3]  into how many parts k is split (1: it is whole)
+ *   path[4]  few rows, tiles: values of k in a step
+ *   path[5]  tiles: steps in a part of k
+ * and 0 where nothing is named. Limits and errors as moe_linear(), B >= 1.
+ */
+int moed_selftest_linear(int B, int K, int N, int x_dtype, int w_dtype, int32_t *path);
+
+/*
  * Measurement kernels (not part of the layer).
  * moed_bench_read: streams `bytes` from `src` with contiguous 16-byte loads --
  *   the peak-read reference the warp-decode post compares against (section

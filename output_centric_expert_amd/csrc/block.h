@@ -21,6 +21,8 @@ struct LinearArgs {
 };
 size_t linear_workspace(int B, int K, int N, bool x_bf16, bool w_bf16);
 hipError_t launch_linear(const LinearArgs& p, bool x_bf16, bool w_bf16, void* workspace, hipStream_t s);
+// What launch_linear takes: see moed_selftest_linear.
+void linear_path(int B, int K, int N, bool x_bf16, bool w_bf16, int32_t* path);
 
 // The router's choice by scores and groups (route_scored.hip).
 constexpr int kRouteMaxGroups = 64;

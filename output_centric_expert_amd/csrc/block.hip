@@ -54,6 +54,18 @@ size_t moe_linear_workspace_bytes(int B, int K, int N, int x_dtype, int w_dtype)
     return moed::linear_workspace(B, K, N, x_dtype == MOED_BF16, w_dtype == MOED_BF16);
 }
 
+int moed_selftest_linear(int B, int K, int N, int x_dtype, int w_dtype, int32_t* path)
+{
+    if (!linear_ok(B, K, N) || B == 0)
+        return MOED_ERR_SHAPE;
+    if (!dtype_ok(x_dtype) || !dtype_ok(w_dtype))
+        return MOED_ERR_DTYPE;
+    if (!path)
+        return MOED_ERR_NULL;
+    moed::linear_path(B, K, N, x_dtype == MOED_BF16, w_dtype == MOED_BF16, path);
+    return MOED_OK;
+}
+
 int moe_linear(const void* x, int x_dtype, const void* w, int w_dtype, const void* bias, int bias_dtype, int activation,
                const void* residual, int residual_dtype, void* out, int out_dtype, int B, int K, int N, void* workspace,
                size_t workspace_bytes, void* stream)

@@ -93,6 +93,9 @@ struct Choice {
     SkinnyPlan skinny_plan;
 };
 
+// Values of k in a step of the skinny kernel.
+int skinny_step(bool x_bf16, bool w_bf16) { return !x_bf16 && !w_bf16 ? 32 : 64; }
+
 bool tile_cost(bool x_bf16, bool w_bf16, int tile, TileCost* t)
 {
     return x_bf16 ? (w_bf16 ? linear_cost_bf16(tile, t) : linear_cost_mixed_w(tile, t))
@@ -110,7 +113,7 @@ Choice choose(int B, int K, int N, bool x_bf16, bool w_bf16)
         c.kind = Choice::dot;
         return c;
     }
-    const int step = !x_bf16 && !w_bf16 ? 32 : 64;
+    const int step = skinny_step(x_bf16, w_bf16);
     {
         c.swapped = N < B;
         const int few = c.swapped ? N : B, many = c.swapped ? B : N;
@@ -171,6 +174,21 @@ size_t linear_workspace(int B, int K, int N, bool x_bf16, bool w_bf16)
 {
     const Choice c = choose(B, K, N, x_bf16, w_bf16);
     return c.splits > 1 ? (size_t)c.splits * (size_t)B * (size_t)N * 4 : 0;
+}
+
+void linear_path(int B, int K, int N, bool x_bf16, bool w_bf16, int32_t* path)
+{
+    const Choice c = choose(B, K, N, x_bf16, w_bf16);
+    const bool tiled = c.kind == Choice::tiled, skinny = c.kind == Choice::skinny;
+    TileCost t = {};
+    if (tiled)
+        tile_cost(x_bf16, w_bf16, c.tile, &t);
+    path[0] = skinny ? 1 : tiled ? 2 : 0;
+    path[1] = skinny ? c.rt : tiled ? c.tile : 0;
+    path[2] = skinny && c.swapped;
+    path[3] = c.splits;
+    path[4] = skinny ? skinny_step(x_bf16, w_bf16) : t.k;
+    path[5] = tiled ? c.plan.split_steps : 0;
 }
 
 namespace {

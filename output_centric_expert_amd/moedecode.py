@@ -29,7 +29,7 @@ EXPORTS = ("moed_workspace_bytes", "moe_decode", "moe_decode_gate_up", "moe_deco
            "moe_decode_down_tuned", "moe_decode_noalloc", "moed_bench_read_cfg", "moe_norm",
            "moe_group_workspace_bytes", "moe_group", "moe_grouped_workspace_bytes", "moe_grouped_gate_up",
            "moe_grouped_matmul", "moe_combine", "moe_prefill_workspace_bytes", "moe_prefill",
-           "moe_linear_workspace_bytes", "moe_linear", "moe_route_scored", "moe_post_norm")
+           "moe_linear_workspace_bytes", "moe_linear", "moe_route_scored", "moe_post_norm", "moed_selftest_linear")
 
 
 class MoedTuning(ctypes.Structure):
@@ -109,6 +109,8 @@ def load() -> ctypes.CDLL:
         lib.moe_post_norm.restype = I
         lib.moed_selftest_decode.argtypes = [P, P, P, I, I, P]
         lib.moed_selftest_decode.restype = I
+        lib.moed_selftest_linear.argtypes = [I] * 5 + [P]
+        lib.moed_selftest_linear.restype = I
         lib.moed_bench_read.argtypes = [P, Z, P, Z, P]
         lib.moed_bench_read.restype = I
         lib.moed_bench_read_cfg.argtypes = [P, Z, P, Z, I, I, I, P]
@@ -762,6 +764,14 @@ def moed_selftest_decode(codes, scales, path: int, out=None, stream=None):
                                      _ptr(out, "out", torch.float32), n, path, _stream(stream))
     _check(st, "moed_selftest_decode")
     return out
+
+
+def moed_selftest_linear(B: int, K: int, N: int, x_dtype=torch.bfloat16, w_dtype=torch.bfloat16):
+    """Which kernel moe_linear takes: (kernel, shape, swapped, splits, values of k in a step, steps in a part of k), as in the
+    header."""
+    path = (ctypes.c_int32 * 6)()
+    _check(load().moed_selftest_linear(B, K, N, _DT[x_dtype], _DT[w_dtype], path), "moed_selftest_linear")
+    return tuple(path)
 
 
 def moed_bench_read(src: torch.Tensor, sink: torch.Tensor, nbytes: int | None = None, stream=None):

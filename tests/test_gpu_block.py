@@ -70,7 +70,8 @@ SIZES = [(1, 1, 1), (1, 2048, 128), (1, 7168, 256), (2, 33, 5), (3, 1111, 777), 
          (8, 2048, 512), (9, 512, 16), (16, 7168, 256), (17, 63, 65), (31, 2049, 130), (32, 4096, 1024), (33, 64, 33),
          (64, 7168, 256), (65, 200, 257), (127, 1000, 96), (128, 128, 128), (200, 20000, 40), (256, 256, 512), (300, 1, 300),
          (1000, 1111, 777), (513, 4104, 520), (2048, 96, 8), (2500, 7, 3), (1024, 1024, 1024), (4096, 520, 264), (4100, 264, 4100), (4100, 77, 4099),
-         # each tile with K even and odd, with k whole and split, steps that end behind K and that do not
+         # tiles with K even and odd, with k whole and split, steps that end behind K and that do not (not every way of
+         # every tile: linear_paths.py has the rest)
          (4090, 712, 4093), (4090, 711, 4093), (4096, 256, 4096), (3161, 37, 2629), (4272, 34, 899), (3692, 33, 1028),
          (2052, 2877, 900), (3422, 34, 546), (647, 33, 2967), (4107, 2212, 35), (3291, 2871, 34), (34, 34, 3285), (33, 33, 3425),
          (36, 998, 3244), (3225, 1189, 33), (2369, 33, 1717), (133, 2816, 3586), (3943, 2765, 130), (3491, 850, 33),
