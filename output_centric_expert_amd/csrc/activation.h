@@ -1,7 +1,8 @@
 // Activations of the dense product and gates of the norm behind a block, in float32, on the hardware's base-2 exponential
-// and reciprocal (one unit in the last place each; the argument's rounding makes (|v| + 3) 2^-24 of a sigmoid at most).
-// The epilogue of a product is bound by these instructions: five for a SiLU. An exponential past float32's range makes the
-// reciprocal 0.
+// and reciprocal (one unit in the last place each). A sigmoid is off by (1.23 |v| + 5) 2^-24 of itself at most: the constant
+// log2(e) by 0.23, its product with v by one, both of them |v| times in the exponential; exponential and reciprocal by two
+// each, the sum by one. The epilogue of a product is bound by these instructions: five for a SiLU. Where the reciprocal is
+// below 2^-126 (v < -87.3) it is 0, also where the exponential passes float32's range.
 #pragma once
 
 #include "block.h"
