@@ -498,11 +498,15 @@ typedef enum {
  *   activation  a moed_activation
  * K and N are any positive numbers (router logits: N experts; a shared
  * expert's gate: N = 1). Sums are float32 of exact products; float32 operands
- * keep float32 precision: above a few rows they enter the matrix instructions
+ * keep float32 precision: from two rows on they enter the matrix instructions
  * as three bfloat16 parts whose sum is the value (products of two float32
- * values leave out the parts below 2^-23 of the product). Where x or w holds an
- * infinity, a NaN or a float32 value that rounds to an infinite bfloat16
- * (3.39e38 and more), the outputs that it enters are infinite or NaN.
+ * values leave out the parts below 2^-23 of the product). A float32 value below
+ * 2^-110 is then taken to within 2^-134. Where x or w holds an infinity, a NaN
+ * or, from two rows on, a float32 value that rounds to an infinite bfloat16
+ * (3.39e38 and more), the outputs that it enters are infinite or NaN: one row
+ * gives the infinity of the sum, parts of an infinity may cancel to NaN.
+ * Where a sigmoid, or the one in SiLU and tanh-GELU, or erfc in GELU is below
+ * 2^-126 it may be 0.
  * A row's low bits can differ between calls of different sizes.
  * workspace: at least moe_linear_workspace_bytes(...) bytes (0 for invalid
  * arguments), 16-byte aligned; NULL where that is 0.
