@@ -12,9 +12,10 @@ constexpr int kDotWaves = 4;
 }  // namespace
 
 // One row of x. A workgroup's four wavefronts share an output's k; their lanes take pieces of 8 neighbouring values, so that
-// a load of a row is contiguous over the wavefront. Bound by the weights' way from memory (4096 x 4096 bfloat16 8.7 us,
-// 3.9 TB/s, of which the launch is 2) and, with few outputs, by one round trip (2048 -> 128 float32: 3.4-4.2 us, the
-// kernel of few rows 6.2: it has 8 workgroups for it, this one 128).
+// a load of a row is contiguous over the wavefront. Bound by the weights' way from memory (4096 x 4096 bfloat16 in a graph
+// 8.4 us from the Infinity Cache, 4.0 TB/s, 9.8-10.2 from HBM; a row's second piece is asked for behind the first one's
+// sum, and the kernel of few rows takes 8.1 where this one takes 8.6) and, with few outputs, by one round trip (2048 -> 128
+// float32: 2.6 us, the kernel of few rows 5.1: it has 8 workgroups for it, this one 128).
 template <bool XBF16, bool WBF16>
 __global__ void __launch_bounds__(kDotWaves * kWave)
 moe_linear_dot_kernel(LinearArgs p)
@@ -79,7 +80,8 @@ moe_linear_join_kernel(LinearArgs p, const float* partial, int splits, unsigned 
 namespace {
 
 // Tiles up to which a product of more than 16 rows is a skinny one: beyond, the chip is full of workgroups that load the same
-// rows. Mixed types, K = 7168: 64 tiles 10.6 us, with the other kernel 12.4; bfloat16, K = 4096: 512 tiles 14.4 and 13.8.
+// rows. 256 x 7168 -> 256, w float32, 128 tiles: 12.8 us, with the other kernel 14.3; 64 x 4096 -> 4096 bfloat16, 512
+// tiles: 15.4 and 14.7.
 constexpr int kSkinnyTiles = 400;
 // A wavefront's us a step of the skinny kernel, by the number of float32 operands (two: steps of 32 values, else of 64).
 constexpr float kSkinnyStep[3] = {0.26f, 0.50f, 0.40f};
@@ -117,8 +119,8 @@ Choice choose(int B, int K, int N, bool x_bf16, bool w_bf16)
     {
         c.swapped = N < B;
         const int few = c.swapped ? N : B, many = c.swapped ? B : N;
-        // 16 x 16 outputs a workgroup where each has a CU of its own then: 32 x 1024 -> 1024 float32 6.2 us (32 x 16: 7.5),
-        // 64 x 4096 -> 1024 bfloat16 6.8 (8.1). Beyond, 32 x 16, which read the side with many half as often.
+        // 16 x 16 outputs a workgroup where each has a CU of its own then: 32 x 1024 -> 1024 float32 5.5 us (32 x 16: 6.8),
+        // 64 x 4096 -> 1024 bfloat16 6.1 (7.5). Beyond, 32 x 16, which read the side with many half as often.
         c.rt = few <= 16 || (long long)((few + 15) / 16) * ((many + 15) / 16) <= 256 ? 1 : 2;
         SkinnyPlan& s = c.skinny_plan;
         s.few_blocks = (few + 16 * c.rt - 1) / (16 * c.rt);
@@ -127,9 +129,9 @@ Choice choose(int B, int K, int N, bool x_bf16, bool w_bf16)
         if (few <= 16 || tiles <= kSkinnyTiles) {
             c.kind = Choice::skinny;
             // k is split where that saves more than a second launch costs, which the host feels more than the GPU: workgroups
-            // for the whole chip then, but a step and a half at least for a wavefront. 16 rows, 256 outputs, bfloat16:
-            // K = 4096 5.3 us whole and 6.7 split, 7168 8.5 and 7.7, 8192 8.8 and 7.9; 64 rows, float32 w: K = 4096 8.7 and
-            // 8.1, 7168 12.0 and 9.5; float32: K = 2048 7.2 and 7.1, 7168 17.6 and 10.7.
+            // for the whole chip then, but a step and a half at least for a wavefront. us of the GPU, 16 rows, 256 outputs,
+            // bfloat16: K = 4096 4.7 whole and 6.1 split, 7168 8.0 and 6.8, 8192 8.3 and 7.1; 64 rows, float32 w: K = 4096
+            // 8.2 and 7.5, 7168 11.4 and 8.9; float32: K = 2048 7.5 and 6.1, 7168 17.2 and 9.9.
             const int steps = (K + step - 1) / step;
             const float whole = (float)steps / kSkinnyWaves * kSkinnyStep[(x_bf16 ? 0 : 1) + (w_bf16 ? 0 : 1)];
             long long splits = 256 / tiles;
@@ -195,7 +197,9 @@ namespace {
 
 hipError_t launch_join(const LinearArgs& p, const float* partial, int splits, hipStream_t s)
 {
-    // 2^20 outputs: 25.3 us with 8 a thread, 26.1 with one (256 x 4096 x 4096 bfloat16); 2^19: 18.2 and 17.9; 2^14: 10.2 and 9.0
+    // The whole product in us with 8 a thread and with one: 256 x 4096 -> 4096 bfloat16 (2^20 outputs) 24.5 and 25.1,
+    // 256 x 7168 -> 8192 (2^21) 63.5 and 64.5, 8192 x 7168 -> 256 with float32 w (2^21) 91 either way; 128 x 4096 -> 4096
+    // (2^19) 17.8 and 17.5, 64 x 7168 -> 256 with float32 w (2^14) 9.2 and 8.7.
     if ((size_t)p.B * (size_t)p.N >= 1u << 20) {
         const unsigned threads = (unsigned)p.B * (((unsigned)p.N + 7) / 8);
         hipLaunchKernelGGL(moe_linear_join_kernel<8>, dim3((threads + 255) / 256), dim3(256), 0, s, p, partial, splits, threads);

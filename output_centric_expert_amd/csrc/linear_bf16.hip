@@ -6,11 +6,11 @@ namespace moed {
 
 namespace {
 
-// us with each of the four, k split as suits it best (float32 out):
-//   8192 x 4096 x 4096   248  285  378  449     the larger the tile, the fewer bytes through LDS for a product
-//   2048 x 4096 x 4096    85   73   98  116     256 of the second
-//   1024 x 1024 x 4096  33.1 23.8 17.6 21.3     512 of the third, two to a CU
-//   1024 x 1024 x 1024  25.9 20.4 11.9 11.0     the last: the third's with more wavefronts and a fourth buffer
+// us with each of the four, k split as suits it best (float32 out; rows x K -> outputs):
+//   8192 x 4096 -> 4096   226  275  373  448     the larger the tile, the fewer bytes through LDS for a product
+//   2048 x 4096 -> 4096    84   75   99  115     256 of the second
+//   1024 x 1024 -> 4096  32.7 23.2 16.7 20.0     512 of the third, two to a CU
+//   1024 x 1024 -> 1024  25.4 20.0 11.3 10.4     the last: the third's with more wavefronts and a fourth buffer
 constexpr TileCost kTiles[] = {
     {256, 256, 64, 1.67f, 0.00f},
     {128, 256, 64, 1.00f, 0.00f},

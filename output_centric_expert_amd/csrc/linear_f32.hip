@@ -6,8 +6,8 @@ namespace moed {
 
 namespace {
 
-// us with each of the three: 4096 x 4096 x 4096 622, 877, 1046 (both sides split once for 256 and 128 rows of the other);
-// 2000 x 300 x 1000 30.4, 16.8, 21.5 (two of the second to a CU); 1024 x 1024 x 1024 34.4, 26.1, 21.6 (one to a CU: half as
+// us with each of the three: 4096 x 4096 -> 4096 579, 876, 1039 (both sides split once for 256 and 128 rows of the other);
+// 2000 x 300 -> 1000 28.2, 16.4, 20.8 (two of the second to a CU); 1024 x 1024 -> 1024 32.6, 25.7, 20.9 (one to a CU: half as
 // many barriers).
 constexpr TileCost kTiles[] = {
     {256, 128, 32, 2.40f, 0.00f},

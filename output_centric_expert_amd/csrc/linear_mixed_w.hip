@@ -6,8 +6,8 @@ namespace moed {
 
 namespace {
 
-// us with either (float32 out): 8192 x 4096 x 4096 650 and 1055, 8192 x 7168 x 256 89 and 134, 2048 x 2048 x 1024 40.6 and
-// 39.2, 1024 x 1024 x 1024 29.8 and 17.1. w's rows are split once for 256 rows of x in the first; the second fills the chip.
+// us with either (float32 out): 8192 x 4096 -> 4096 611 and 1050, 8192 x 7168 -> 256 89 and 132, 2048 x 2048 -> 1024 39.9 and
+// 37.8, 1024 x 1024 -> 1024 28.3 and 16.4. w's rows are split once for 256 rows of x in the first; the second fills the chip.
 constexpr TileCost kTiles[] = {
     {256, 128, 64, 2.45f, 0.00f},
     {64, 64, 64, 0.80f, 1.05f}};

@@ -6,8 +6,8 @@ namespace moed {
 
 namespace {
 
-// us with either (float32 out): 8192 x 4096 x 4096 658 and 779, 8192 x 7168 x 256 92 and 101, 2048 x 2048 x 1024 40.7 and
-// 36.1, 1024 x 1024 x 1024 30.5 and 19.5. x's rows are split once for 256 rows of w in the first; the second fills the chip.
+// us with either (float32 out): 8192 x 4096 -> 4096 636 and 781, 8192 x 7168 -> 256 97 and 108, 2048 x 2048 -> 1024 38.3 and
+// 35.2, 1024 x 1024 -> 1024 29.9 and 18.7. x's rows are split once for 256 rows of w in the first; the second fills the chip.
 constexpr TileCost kTiles[] = {
     {128, 256, 64, 2.60f, 0.00f},
     {64, 128, 64, 0.95f, 1.50f}};

@@ -6,13 +6,16 @@
 // ring of LDS of its own that its loads fill and its fragments are read from: no barrier before the sums are added, in
 // the order of the wavefronts, and the epilogue.
 //
-// Bound by the way of the rows from memory, and for short products by one round trip of it, the sum and the launch:
+// Bound by the way of the rows from memory, and for short products by one round trip of it, the sum and the launch (us a
+// call in a graph, eight sets of inputs in turn):
 //                                          here    the tiles' kernel
-//   32 x 4096 -> 4096 bfloat16             10.6 us   13.3             (3.2 TB/s)
-//   16 x 2048 -> 512 bfloat16               4.4       8.4
-//   64 x 7168 -> 256, w float32             9.5      13.3             (both with k split and a second launch)
-//   8192 x 4096 -> 16 bfloat16             18.9      19.9             (3.6 TB/s)
-// There a barrier a step lets the wavefronts wait together; here others' loads fill in for one's wait.
+//   32 x 4096 -> 4096 bfloat16             10.1      12.9
+//   16 x 2048 -> 512 bfloat16               3.8       7.8
+//   64 x 7168 -> 256, w float32             8.8      12.6             (both with k split and a second launch)
+//   8192 x 4096 -> 16 bfloat16             18.6      19.2
+// There a barrier a step lets the wavefronts wait together; here others' loads fill in for one's wait. Two sets of inputs
+// stay in the Infinity Cache: 8.9 us for the first of these (3.9 TB/s) and 14.0 for the last (4.8); from HBM, with sixteen,
+// 11.4-12.6 and 18.4 (2.7-3.0 and 3.7).
 #pragma once
 
 #include <type_traits>
@@ -176,7 +179,8 @@ moe_linear_skinny_kernel(LinearArgs p, SkinnyPlan plan)
         }
         slot = slot + 1 == S::kRing ? 0 : slot + 1;
     }
-    // sums of the wavefronts: [wavefront][few][many]
+    // Sums of the wavefronts: [wavefront][few][many]. Their 16-byte writes are all of the kernel's LDS bank conflicts, 24
+    // cycles a fragment whatever K (18 % of its LDS cycles at 32 x 4096 -> 4096, 6 % at K = 16384).
     float* const sums = reinterpret_cast<float*>(lds + w * (S::kRing * S::kSlot));
     wave_lds_fence();
 #pragma unroll

@@ -8,10 +8,13 @@
 // third (a sixth) of the bfloat16 rate; the float32 matrix instructions have a sixteenth.
 //
 // What bounds it, with the chip full: the matrix instructions and the loads' way into LDS, which do not overlap all the time
-// (the matrix unit is busy for half of it). A step of a 256 x 256 bfloat16 tile is 64 KiB in and 8.4 MFLOP. Measured:
-//   bfloat16 x bfloat16  8192 x 8192 x 8192 794 us (1.38 PFLOP/s); 8192 x 4096 x 4096 220 us, with bias, SiLU and residual 234
-//   bfloat16 x float32   8192 x 4096 x 4096 622 us (1.33 PFLOP/s of the three products)
-//   float32 x float32    4096 x 4096 x 4096 582-596 us (1.38-1.42 PFLOP/s of the six)
+// (the matrix unit is busy for half of it). A step of a 256 x 256 bfloat16 tile is 64 KiB in and 8.4 MFLOP. Measured, fastest
+// and median of a graph of calls (the chip slows down while they follow one another):
+//   bfloat16 x bfloat16  8192 x 8192 x 8192 813-831 us (1.32-1.35 PFLOP/s); 8192 x 4096 x 4096 215-226, with bias, SiLU and
+//                        residual 233-245
+//   bfloat16 x float32   8192 x 4096 x 4096 602-621 us (1.33-1.37 PFLOP/s of the three products)
+//   float32 x bfloat16   8192 x 4096 x 4096 620-645 us (1.28-1.33)
+//   float32 x float32    4096 x 4096 x 4096 564-583 us (1.41-1.46 PFLOP/s of the six)
 // Smaller products are bound by what a step takes on a CU with little of its own work: the trip to LDS and the barrier.
 #pragma once
 
@@ -478,7 +481,10 @@ moe_linear_tiled_kernel(LinearArgs p, LinearPlan plan)
 }
 
 // A tile that a pair of types has, and what a step of it takes in us, as measured where all 256 CUs have one (or two) of
-// them: products of 1024 to 8192 rows and K = 4096, less 4 us for the beginning and the end.
+// them: products of 1024 to 8192 rows and K = 4096, less 4 us for the beginning and the end. The large tiles with a float32
+// operand are 3 to 6 % faster than their number here, which is from before their wavefronts took turns (today's would be
+// 2.25 of float32, 2.37 and 2.47 of one float32 side), and not every size gets its best tile: float32 1400 x 1024 -> 1024 has
+// 35.3 us and could have 33.0, bfloat16 700 x 4096 -> 4096 51.6 and 46.5, 2048 x 2048 -> 1024 with float32 w 40.1 and 37.8.
 struct TileCost {
     int rows, outputs, k;   // of x, of w, of a step
     float alone, paired;    // with one workgroup a CU, and with two (0: there is no room for two)

@@ -8,8 +8,8 @@
 // A row stays in the registers of its threads (8 values a piece, NV pieces a thread, TPR threads a row) from the loads to
 // the last store; two sums over the row stand between them. All loads are asked for in front of the first use of any
 // (raw: a conversion behind a load waits for it), so that a row waits for memory once, twice where its rows' places
-// come first. Memory bound: 8192 tokens of 4096 values, bfloat16, with MXFP8 55-57 us (5.4 TB/s), 8 expert rows a token of
-// 2048 and a float32 residual 76 us (5.7 TB/s; 105 with conversions between the loads), rows of 1111 values 24 us (3 TB/s:
+// come first. Memory bound: 8192 tokens of 4096 values, bfloat16, with MXFP8 55-59 us (5.1-5.5 TB/s), 8 expert rows a token of
+// 2048 and a float32 residual 76-78 us (5.6 TB/s; 105 with conversions between the loads), rows of 1111 values 24 us (3 TB/s:
 // their pieces begin at any element, and their stores do not fill lines); one token 3-4 us, two round trips and the launch.
 // Rows may begin at any element and have any length: a piece that would pass the row's end is the row's last 8 values
 // instead, of which the first `skip` are another piece's: loaded, but neither counted nor stored.
@@ -315,7 +315,8 @@ hipError_t launch_post_norm(const PostNormArgs& p, bool y_bf16, bool residual_bf
         return launch_shape<2, 64>(p, y_bf16, residual_bf16, s);
     if (p.H <= 2048)
         return launch_shape<1, 256>(p, y_bf16, residual_bf16, s);
-    // few rows: more threads a row (one token of 4096 values 4.3 us instead of 6.0; 8192 of 4095 values 66 instead of 61)
+    // few rows: more threads a row (one token of 4096 values 3.6 us, with 256 threads 4.3; 512 tokens 6.2 and 6.7, 8192 of
+    // 4095 values 65.6 and 59.4)
     if (p.H <= 4096 && p.B < 512)
         return launch_shape<1, 512>(p, y_bf16, residual_bf16, s);
     if (p.H <= 4096)

@@ -9,9 +9,10 @@
 //
 // L lanes own a token, NPL neighbouring experts each (expert = lane * NPL + t), so that among equal keys the lowest
 // lane, and in it the lowest t, is the lowest expert. A key is the order-preserving map of the choice to 32 bits; 0: not
-// to be chosen. What bounds it is the vector unit with many tokens (16384 of 256 experts, 8 of 4 of 8 groups: 14-15 us for
-// 1411 instructions a wavefront, which are 9.4 us of issue; its bytes are 3), one round trip to memory and the rounds' chain
-// with few (1 token of 128 experts 3.7-4.2 us, 64 of 256 5.6). So there are two kernels:
+// to be chosen. What bounds it is the vector unit with many tokens (16384 of 256 experts, 8 of 4 of 8 groups: 14.3-15.2 us a
+// call in a graph, 13.4 of calls that overlap, for 1411 instructions a wavefront, which are 9.4 us of issue; its bytes are
+// 3), one round trip to memory and the rounds' chain with few (1 token of 128 experts 4.1 us, 64 of 256 5.4). So there are
+// two kernels:
 //  - few tokens, many experts or k: a token a wavefront. Round j takes the largest key of the lanes (DPP), the lowest
 //    lane that holds it writes the expert to the token's list in LDS and clears its key.
 //  - many tokens: 16 lanes a token, four tokens a wavefront. Key and expert are packed into one float64 (43 bits, the lower
@@ -535,8 +536,15 @@ hipError_t launch_many(const RouteArgs& p, hipStream_t s)
 
 hipError_t launch_route_scored(const RouteArgs& p, hipStream_t s)
 {
-    // 256 experts, 8 of 4 of 8 groups, us with a wavefront a token and with 16 lanes: 1024 tokens 5.9 and 6.6, 2048 6.4 and 6.6,
-    // 4096 8.5 and 6.8, 16384 22.7 and 15.0. 128 experts without groups, 1024 4.9 and 5.1, 16384 15.6 and 9.8.
+    // us with a wavefront a token and with 16 lanes:
+    //   tokens                              1024         2048         4096        16384
+    //   8 of 256 experts, 4 of 8 groups   5.6   6.3    6.2   6.4    8.4   6.5    22.4  14.3
+    //   8 of 256                          4.7   5.6    5.3   5.7    7.0   5.8    18.5  13.1
+    //   2 of 256                          3.5   5.4    3.9   5.5    4.9   5.7    12.2  12.8    two rounds only
+    //   8 of 128                          4.3   4.2    4.7   4.3    5.8   4.4    14.0   8.8
+    //   8 of 64                           4.0   3.8    4.1   3.8    4.9   3.9    10.7   6.5
+    // What goes to the first kernel however many tokens: 8 of 384 experts 7.0, 10.2 and 27.4 us for 2048, 4096 and 16384,
+    // 10 of 512 7.3, 10.9 and 29.1, 12 of 256 6.1, 8.2 and 21.5.
     if (p.B >= 2048 && p.k <= kManyK && p.E <= 256 && p.n_group <= 16) {
         if (p.E <= 64)
             return launch_many<4>(p, s);

@@ -57,8 +57,9 @@ __device__ __forceinline__ void store_vals(void* p, size_t at, const float (&v)[
 // Squares of a row whose sum is below 2^-80 (all |s| < 2^-40) may underflow, and its reciprocal root may pass
 // float32's range. With an eps as small (TINY) the row is then taken times 2^100, and eps times 2^200, which changes
 // nothing else: values from the smallest subnormal number to 2^60, their squares from 2^-98 to 2^120. Above, what is
-// lost to underflow is at most 2^15 squares below 2^-126 each: 2^-31 of the sum, or of eps. A kernel of its own, because
-// the test costs the others: a token of 2048 2.19 instead of 2.10 us, 8192 tokens of 2049 112.7 instead of 110.1.
+// lost to underflow is at most 2^15 squares below 2^-126 each: 2^-31 of the sum, or of eps. moe_norm has a kernel of its own
+// for such an eps, because the test costs the others: a token of 2048 2.19 instead of 2.10 us, 8192 tokens of 2049 112.7
+// instead of 110.1. moe_post_norm, with two norms and an eps of each, tests at run time.
 constexpr float kSmall = 0x1p-80f, kLift = 0x1p100f;
 
 // Sum over the threads of a row (one wavefront, or all of the workgroup), in every one of them.
